@@ -43,6 +43,7 @@
 #ifndef NVFP4_H
 #define NVFP4_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -384,6 +385,111 @@ int nvfp4_attention_fused_splits(int64_t H, int64_t Tq, int64_t Tk, int* splits)
  * (4 H Tq splits (D + 1)), rounded up to 256, plus K, V^T and Q in FP16 ((2 Tk + Tq) H D 2 bytes); 0 for
  * invalid arguments.  Host only. */
 size_t nvfp4_attention_fused_workspace_bytes(int64_t H, int64_t Tq, int64_t Tk, int splits);
+
+/* ---- Decode: attention over the cache, rotary positions, cache pages ---- */
+
+/* One side (K or V) of a mixed-precision cache, as nvfp4_kv_mixed lays it out and nvfp4_kv_append fills it
+ * ("Search your block floating-point scales!", ScaleSearchAttention > attention-sink-aware mixed-precision
+ * caching).  All device memory. */
+typedef struct nvfp4_kv_store {
+  const void* sink;         /* BF16 [slots, Hkv, sink_rows, D]; 16-byte aligned; unused when sink_rows == 0 */
+  const void* window;       /* BF16 ring [slots, Hkv, window_rows, D]; 16-byte aligned; unused when window_rows == 0 */
+  const uint8_t* codes;     /* NVFP4 middle [pages, Hkv, page_rows, D/2]; 16-byte aligned */
+  const uint8_t* scales;    /* [pages, Hkv, page_rows, D/16], or pages * Hkv matrices [page_rows, D] in the tile
+                               layout when scale_layout == 1; 4-byte aligned */
+  const float* gscale;      /* the tensor scale: one float, or one per slot when gscale_stride == 1 */
+  int64_t gscale_stride;    /* 0 or 1 */
+  int32_t rotate;           /* 1: the middle is rotated by FWHT-16 along D (undone by the attention) */
+  int32_t scale_layout;
+} nvfp4_kv_store;
+
+/* Attention of the newest Tq tokens of B sequences over their cached tokens (those Tq included). */
+typedef struct nvfp4_kv_attention_desc {
+  const void* q;            /* [B, Hq, Tq, D] at the given strides (elements; channels contiguous), dtype */
+  void* out;                /* the same shape and dtype at its own strides; must not overlap q */
+  float* lse;               /* NULL, or [B, Hq, Tq] contiguous: log of the softmax denominators (natural log) */
+  int64_t q_sb, q_sh, q_st, out_sb, out_sh, out_st;
+  int64_t B, Hq, Hkv, Tq, D;          /* D: 64, 128 or 256; Hq a multiple of Hkv: query head h reads K/V head
+                                         h / (Hq / Hkv) */
+  nvfp4_kv_store k, v;
+  int64_t slots, sink_rows, window_rows;
+  int64_t pages, page_rows, table_cols;
+  const int32_t* slot;      /* device [B]: the slot of each sequence; NULL: sequence b is slot b (B <= slots).
+                               A value outside [0, slots) is an empty sequence (padding of a batch) */
+  const int32_t* table;     /* device [slots, table_cols]: page of middle tokens [j page_rows, (j + 1) page_rows);
+                               page_rows then is a multiple of 16.  A value outside [0, pages) hides its tokens.
+                               NULL: slot s owns page s, of page_rows tokens (a contiguous cache) */
+  const int32_t* lens;      /* device [slots, 4]: n_sink, n_mid, head, n_window of each slot (bounded by the
+                               buffers' sizes in the kernel); NULL: the four values below for every slot */
+  int32_t n_sink, n_mid, head, n_window;
+  int32_t dtype;            /* NVFP4_BF16 or NVFP4_F16 */
+  int32_t causal;           /* 1: query i of Tq sees the tokens at positions <= n - Tq + i, n the sequence's
+                               length; 0: every token */
+  float scale;              /* multiplies q . k */
+} nvfp4_kv_attention_desc;
+
+/* out = softmax(scale q K^T) V over the tokens of each sequence in the order sink | middle | window (slots head,
+ * head + 1, ... of the ring).  A row that sees no token gets zeros and lse -Inf.  Middle tokens stand for
+ * E2M1(code) * E4M3(scale) * g, un-rotated when `rotate`; sums and softmax statistics are FP32, the middle's
+ * query is carried in 22 bits and its numerators in FP16 (scaled by 2^15), the BF16 ends' in 16 bits.
+ * Hidden tokens (past a row's position, past a sequence's end) reach no row, whatever they hold; a visible
+ * NaN reaches the rows that see it.
+ * splits: 1 .. 128 ranges of the middle per sequence, worked on by different CTAs and then joined by a second
+ * kernel (nvfp4_kv_attention_splits gives a count that fills the current device; any count gives a valid
+ * result, which depends on it in the last bits).  workspace: caller-owned device memory, 16-byte aligned, of
+ * nvfp4_kv_attention_workspace_bytes (NULL with splits == 1); calls that share one must be ordered.
+ * No device memory is allocated and no state kept; lengths, slots and table are read on the device, so a
+ * captured call follows their contents.  NVFP4_ERR_SIZE for unsupported sizes, NVFP4_ERR_ARG for host lengths
+ * outside the buffers. */
+int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* The number of ranges for nvfp4_kv_attention that fills the current device: rows = (Hq / Hkv) * Tq, max_mid an
+ * upper bound on the middle's length (a longer sequence stays correct).  Host only (queries the device). */
+int nvfp4_kv_attention_splits(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t max_mid, int* splits);
+
+/* Bytes of workspace: B * Hkv * rows * splits FP32 accumulators of D channels and two statistics; 0 for one range
+ * or invalid arguments.  Host only. */
+size_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int splits);
+
+/* One tensor of a rotary call: x and out [B, heads, T, D] at the given strides (elements; channels contiguous).
+ * out may be x itself (the same strides, NVFP4_ERR_ARG otherwise) but must not overlap any x otherwise. */
+typedef struct nvfp4_rope_tensor {
+  const void* x;
+  void* out;
+  int64_t heads;
+  int64_t x_sb, x_sh, x_st, out_sb, out_sh, out_st;
+} nvfp4_rope_tensor;
+
+#define NVFP4_ROPE_MAX 8
+
+/* Rotary positions for `count` (at most NVFP4_ROPE_MAX) tensors of one step, e.g. q and k, in one launch: pair i of the
+ * first `rot` channels -- (i, i + rot/2), or (2i, 2i + 1) when interleaved -- turns by position * freqs[i]
+ * radians and is multiplied by mscale; channels from `rot` on pass unchanged.  inverse = 1 turns by the
+ * negative angle: with the same mscale the adjoint, which is the gradient's pass.
+ * positions: device int32 (positions64 == 0) or int64, that of token t of sequence b at b * pos_sb + t * pos_st;
+ * freqs: device, rot / 2 doubles (angles are formed in FP64, products in FP32, one rounding to dtype).
+ * rot even, 0 <= rot <= D, rot <= 1024, D - rot even when interleaved (NVFP4_ERR_SIZE otherwise).  16-byte aligned
+ * rows move in 16-byte pieces, others element by element.  The pages have no counterpart. */
+int nvfp4_rope(const nvfp4_rope_tensor* tensors, int count, int64_t B, int64_t T, int64_t D, int64_t rot, int interleaved,
+               int dtype, const void* positions, int positions64, int64_t pos_sb, int64_t pos_st, const double* freqs,
+               float mscale, int inverse, void* stream);
+
+/* One array holding a piece of every page: page i of outer piece o is the `item` bytes at
+ * base + o * stride + i * item, for i < pages (stride >= pages * item). */
+typedef struct nvfp4_pages_array {
+  void* base;               /* device */
+  int64_t outer, stride, item, pages;
+} nvfp4_pages_array;
+
+#define NVFP4_PAGES_MAX 16
+
+/* Copies page src[j] to page dst[j], j < n, in every one of `count` (at most NVFP4_PAGES_MAX) arrays: forking a
+ * sequence, copying on write, compacting a pool.  src and dst are HOST arrays, read before the call returns.
+ * All pairs move at once: every dst is distinct and none of them is a src (NVFP4_ERR_ARG otherwise, as for an
+ * index outside the smallest array's pages; nothing is enqueued).  One launch per 1024 pairs. */
+int nvfp4_copy_pages(const nvfp4_pages_array* arrays, int count, const int32_t* src, const int32_t* dst, int64_t n,
+                     void* stream);
 
 /* Host only, for verification: the byte offsets at which nvfp4_gemm_nt reads the scale of (matrix l,
  * row r, block column c), for l < batch, r < rows, c < K/16 in that (row-major) order, into out

@@ -9,7 +9,9 @@ Element types: torch.float32, torch.bfloat16, torch.float16.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import math
 import numbers
 import os
 
@@ -20,6 +22,7 @@ __all__ = [
     "dequantize", "quantize_dequantize", "hadamard16", "kv_mixed", "kv_mixed_dequantize", "DTYPE_CODE", "sf_mma_bytes", "quantize_mma", "quantize_mma_t", "kv_mixed_mma",
     "gemm_nt", "gemm_sf_offsets", "kv_gscale", "kv_append", "mxfp4_quantize", "mxfp4_dequantize",
     "msda_forward", "softmax_quantize_mma", "rows_divide", "attention_fp4", "search_policy", "kv_append_batch", "KvAppendBatch",
+    "KvStore", "kv_attention", "rope", "rope_frequencies", "copy_pages",
 ]
 
 _SO = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4.so")
@@ -64,6 +67,11 @@ _SIGS = {
                                    _I64, _I, _I, _I, _P, ctypes.c_size_t, _P, _P, _P, _P, _P, _P, _P, _P]),
     "nvfp4_attention_fused_splits": (_I, [_I64, _I64, _I64, _P]),
     "nvfp4_attention_fused_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I]),
+    "nvfp4_kv_attention": (_I, [_P, _I, _P, ctypes.c_size_t, _P]),
+    "nvfp4_kv_attention_splits": (_I, [_I64, _I64, _I64, _I64, _I64, _P]),
+    "nvfp4_kv_attention_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I]),
+    "nvfp4_rope": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I, _I, _P, _I, _I64, _I64, _P, ctypes.c_float, _I, _P]),
+    "nvfp4_copy_pages": (_I, [_P, _I, _P, _P, _I64, _P]),
     "nvfp4_gemm_sf_offsets": (_I, [_I64, _I64, _I64, _P]),
 }
 
@@ -742,3 +750,367 @@ def attention_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
     vc, vsf, vg = quantize_mma_t(v.contiguous(), f_lo, f_hi)
     o = gemm_nt(pc, psf, pg, vc, vsf, vg)
     return rows_divide(o, l)
+
+
+# ---- decode: attention over the cache, rotary positions, cache pages ----
+def _launch(device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) on `device` and its current stream: a kernel is launched on the current device, so
+    that one is switched when the tensors live on another."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
+    """A CUDA tensor that is addressed by strides, its last dimension contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t
+
+
+def _no_shared_elements(t: torch.Tensor, name: str) -> None:
+    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} must not be an expanded tensor (it is written)")
+
+
+def _extent(t: torch.Tensor) -> tuple[int, int]:
+    """First and past-the-last byte that t's elements occupy."""
+    lo = hi = 0
+    for n, s in zip(t.shape, t.stride()):
+        if n == 0:
+            return 0, 0
+        if s < 0:
+            lo += (n - 1) * s
+        else:
+            hi += (n - 1) * s
+    e, p = t.element_size(), t.data_ptr()
+    return p + lo * e, p + (hi + 1) * e
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    (a0, a1), (b0, b1) = _extent(a), _extent(b)
+    return a0 < b1 and b0 < a1
+
+
+class _KvStore(ctypes.Structure):
+    """nvfp4_kv_store (include/nvfp4.h)."""
+    _fields_ = [("sink", _P), ("window", _P), ("codes", _P), ("scales", _P), ("gscale", _P), ("gscale_stride", _I64),
+                ("rotate", ctypes.c_int32), ("scale_layout", ctypes.c_int32)]
+
+
+class _KvAttentionDesc(ctypes.Structure):
+    """nvfp4_kv_attention_desc (include/nvfp4.h)."""
+    _fields_ = [("q", _P), ("out", _P), ("lse", _P),
+                *((n, _I64) for n in ("q_sb", "q_sh", "q_st", "out_sb", "out_sh", "out_st", "B", "Hq", "Hkv", "Tq", "D")),
+                ("k", _KvStore), ("v", _KvStore),
+                *((n, _I64) for n in ("slots", "sink_rows", "window_rows", "pages", "page_rows", "table_cols")),
+                ("slot", _P), ("table", _P), ("lens", _P),
+                *((n, ctypes.c_int32) for n in ("n_sink", "n_mid", "head", "n_window", "dtype", "causal")),
+                ("scale", ctypes.c_float)]
+
+
+class KvStore:
+    """One side (K or V) of a mixed-precision cache as kv_attention reads it, checked once: sink [slots, H, s, D]
+    and window [slots, H, w, D] (BF16; zero rows if there are none), codes uint8 [pages, H, rows, D/2], scales
+    uint8 [pages, H, rows, D/16] (or the tile layout of the pages * H matrices [rows, D]), gscale float32 [1]
+    or [slots].  The tensors are kept alive; their contents are read at each call."""
+
+    def __init__(self, sink: torch.Tensor, window: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                 gscale: torch.Tensor, rotate: bool = True, tile_layout: bool = False):
+        for t, nm in ((sink, "sink"), (window, "window"), (codes, "codes"), (scales, "scales"), (gscale, "gscale")):
+            _cuda(t, nm)
+            if t.device != codes.device:
+                raise ValueError(f"{nm} is on {t.device}, codes on {codes.device}")
+        if sink.dtype != torch.bfloat16 or window.dtype != torch.bfloat16:
+            raise TypeError("sink and window must be bfloat16")
+        if codes.dtype != torch.uint8 or codes.dim() != 4 or sink.dim() != 4 or window.dim() != 4:
+            raise TypeError("codes must be 4-D uint8 [pages, H, rows, D/2], sink and window 4-D [slots, H, rows, D]")
+        pages, H, rows, D = codes.shape[0], codes.shape[1], codes.shape[2], 2 * codes.shape[3]
+        S = sink.shape[0]
+        if sink.shape[1] != H or sink.shape[3] != D or window.shape[:2] != (S, H) or window.shape[3] != D:
+            raise ValueError("sink, window and codes disagree on slots, heads or head_dim")
+        if D % 16:
+            raise ValueError("head_dim must be a multiple of 16")
+        _out(scales, "scales", torch.uint8, sf_mma_bytes(rows, D, pages * H) if tile_layout else pages * H * rows * (D // 16))
+        _out(gscale, "gscale", torch.float32, 1)
+        if gscale.numel() not in (1, S):
+            raise ValueError("gscale must hold one value, or one per slot")
+        self.slots, self.H, self.D, self.pages, self.page_rows = S, H, D, pages, rows
+        self.sink_rows, self.window_rows, self.device = sink.shape[2], window.shape[2], codes.device
+        self.geometry = (S, H, D, pages, rows, self.sink_rows, self.window_rows, codes.device)
+        self._keep = (sink, window, codes, scales, gscale)
+        self._desc = _KvStore(*(t.data_ptr() for t in self._keep), 1 if gscale.numel() > 1 else 0, int(bool(rotate)),
+                              int(bool(tile_layout)))
+
+
+_kv_splits_memo: dict = {}
+
+
+def _kv_splits(device: torch.device, B: int, H: int, rows: int, D: int, max_mid: int) -> tuple[int, int]:
+    """(splits, workspace bytes) that nvfp4_kv_attention_splits gives for these sizes (a pure function of them
+    and the device, remembered)."""
+    key = (device.index, B, H, rows, D, max_mid)
+    got = _kv_splits_memo.get(key)
+    if got is None:
+        s = ctypes.c_int(0)
+        with torch.cuda.device(device):
+            _check(lib().nvfp4_kv_attention_splits(B, H, rows, D, max_mid, ctypes.byref(s)))
+        if len(_kv_splits_memo) > 4096:
+            _kv_splits_memo.clear()
+        got = _kv_splits_memo[key] = (s.value, lib().nvfp4_kv_attention_workspace_bytes(B, H, rows, D, s.value))
+    return got
+
+
+def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Tensor | None = None,
+                 slots: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
+                 max_mid: int | None = None, want_lse: bool = False, out: torch.Tensor | None = None,
+                 lse: torch.Tensor | None = None, splits: int | None = None, workspace: torch.Tensor | None = None):
+    """Attention of the newest Tq tokens of every sequence over its cached tokens (those Tq included), reading the
+    NVFP4 middle where it lies.
+
+    q: bfloat16 / float16 [B, Hq, Tq, D] (any strides, D contiguous), D 64, 128 or 256, Hq a multiple of the
+    stores' H (query head h reads K/V head h // (Hq // H)).
+    lens: (n_sink, n_mid, head, n_window) for every slot, or an int32 device tensor [slots, 4] read by the kernel.
+    table: int32 [slots, cols], the page of each run of `rows` middle tokens (rows a multiple of 16); None: slot s
+    owns page s.  slots: int32 [B], the slot of each batch row (outside [0, slots): an empty sequence); None: row
+    b is slot b.  causal: query i of Tq sees positions <= length - Tq + i.
+    max_mid: a bound on the middle's length that sizes the work split when lens is on the device (any value
+    gives a correct result).  splits / workspace: nvfp4_kv_attention_splits' choice and an own allocation by default.
+    Returns out [B, Hq, Tq, D] in q's dtype, or (out, lse float32 [B, Hq, Tq]) with want_lse."""
+    _rows(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Tq, D]")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("q must be bfloat16 or float16")
+    if not isinstance(k, KvStore) or not isinstance(v, KvStore):
+        raise TypeError("k and v must be KvStore")
+    if k.geometry != v.geometry:
+        raise ValueError("k and v stores disagree on their sizes or device")
+    B, Hq, Tq, D = q.shape
+    dev = q.device
+    if D != k.D or dev != k.device:
+        raise ValueError("q and the stores disagree on head_dim or device")
+    if k.H == 0 or Hq % k.H:
+        raise ValueError("query heads must be a multiple of the K/V heads")
+    rows = Hq // k.H * Tq
+    d = _KvAttentionDesc()
+    most = k.page_rows
+    if table is not None:
+        _cuda(table, "table")
+        if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != k.slots or table.device != dev:
+            raise ValueError("table must be int32 [slots, cols] on q's device")
+        d.table, d.table_cols = table.data_ptr(), table.shape[1]
+        most *= table.shape[1]
+        if table.shape[1] == 0:
+            raise ValueError("table has no columns")
+    elif k.pages < k.slots:
+        raise ValueError("without a table every slot needs its own page")
+    if isinstance(lens, torch.Tensor):
+        _cuda(lens, "lens")
+        if lens.dtype != torch.int32 or lens.shape != (k.slots, 4) or lens.device != dev:
+            raise ValueError("lens must be int32 [slots, 4] on q's device")
+        d.lens = lens.data_ptr()
+        hint = most if max_mid is None else min(max(int(max_mid), 0), most)
+    else:
+        d.n_sink, d.n_mid, d.head, d.n_window = lens
+        hint = int(lens[1])
+    if slots is not None:
+        _cuda(slots, "slots")
+        if slots.dtype != torch.int32 or slots.shape != (B,) or slots.device != dev:
+            raise ValueError("slots must be int32 [B] on q's device")
+        d.slot = slots.data_ptr()
+    elif B > k.slots:
+        raise ValueError("more batch rows than slots")
+    if out is None:
+        out = torch.empty((B, Hq, Tq, D), dtype=q.dtype, device=dev)
+    else:
+        _rows(out, "out")
+        if out.shape != q.shape or out.dtype != q.dtype or out.device != dev:
+            raise ValueError("out must have q's shape, dtype and device")
+        _no_shared_elements(out, "out")
+        if _overlap(out, q):
+            raise ValueError("out must not overlap q")
+    if lse is not None:
+        _out(lse, "lse", torch.float32, B * Hq * Tq)
+        if lse.device != dev:
+            raise ValueError("lse must be on q's device")
+    elif want_lse:
+        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
+    if splits is None:
+        splits, need = _kv_splits(dev, B, k.H, rows, D, max(hint, 0))
+    else:
+        splits = int(splits)
+        need = lib().nvfp4_kv_attention_workspace_bytes(B, k.H, rows, D, splits)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _cuda(workspace, "workspace")
+        if workspace.device != dev or workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace must hold {need} bytes on q's device")
+    d.q, d.out = q.data_ptr(), out.data_ptr()
+    if lse is not None:
+        d.lse = lse.data_ptr()
+    d.q_sb, d.q_sh, d.q_st = q.stride()[:3]
+    d.out_sb, d.out_sh, d.out_st = out.stride()[:3]
+    d.B, d.Hq, d.Hkv, d.Tq, d.D = B, Hq, k.H, Tq, D
+    d.k, d.v = k._desc, v._desc
+    d.slots, d.sink_rows, d.window_rows, d.pages, d.page_rows = k.slots, k.sink_rows, k.window_rows, k.pages, k.page_rows
+    d.dtype, d.causal, d.scale = DTYPE_CODE[q.dtype], int(bool(causal)), D ** -0.5 if scale is None else scale
+    _launch(dev, lib().nvfp4_kv_attention, ctypes.byref(d), splits, None if workspace is None else workspace.data_ptr(),
+            need if workspace is not None else 0)
+    return (out, lse) if want_lse else out
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: dict | None = None, device="cuda") -> tuple[torch.Tensor, float]:
+    """(freqs float64 [rot / 2] in radians per position, mscale) for rope: base^(-2 i / rot), stretched for contexts
+    longer than the trained one by `scaling`:
+      {"type": "linear", "factor"}: every angle divided by factor (arXiv 2306.15595);
+      {"type": "ntk", "factor"}: base * factor^(rot / (rot - 2)), so that the lowest frequency is divided by factor;
+      {"type": "yarn", "factor", "original", "fast": 32, "slow": 1}: pairs that turn more than `fast` times in
+        `original` positions kept, fewer than `slow` divided by factor, a linear ramp over the pairs between;
+        mscale = 0.1 ln(factor) + 1 (arXiv 2309.00071);
+      {"type": "bands", "factor", "original", "low": 1, "high": 4}: the same idea with the ramp linear in the turns."""
+    if rot < 0 or rot % 2:
+        raise ValueError("rot must be even")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    s = dict(scaling or {})
+    kind, factor = s.get("type"), float(s.get("factor", 1.0))
+    if kind not in (None, "linear", "ntk", "yarn", "bands"):
+        raise ValueError(f"unknown scaling type {kind!r}")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must exceed 1 and factor be at least 1")
+    if kind == "ntk":
+        if rot <= 2:
+            raise ValueError("ntk scaling needs rot > 2")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-2.0 * i / max(rot, 1))
+    mscale = 1.0
+    if kind == "linear":
+        f = f / factor
+    elif kind in ("yarn", "bands"):
+        if not float(s.get("original", 0)) > 0:
+            raise ValueError(f"{kind} scaling needs the original context length")
+        n = float(s["original"])
+        if kind == "yarn":
+            def pair(turns):   # the (fractional) pair that turns so often in n positions
+                return rot * math.log(n / (turns * 2 * math.pi)) / (2 * math.log(base))
+            lo = max(math.floor(pair(float(s.get("fast", 32.0)))), 0)
+            hi = min(math.ceil(pair(float(s.get("slow", 1.0)))), rot - 1)
+            cut = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            mscale = 0.1 * math.log(factor) + 1.0
+        else:
+            low, high = float(s.get("low", 1.0)), float(s.get("high", 4.0))
+            if not high > low:
+                raise ValueError("bands scaling needs high > low")
+            cut = 1 - ((n * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f / factor * cut + f * (1 - cut)
+    return f.to(device), mscale
+
+
+class _RopeTensor(ctypes.Structure):
+    """nvfp4_rope_tensor (include/nvfp4.h)."""
+    _fields_ = [("x", _P), ("out", _P), *((n, _I64) for n in ("heads", "x_sb", "x_sh", "x_st", "out_sb", "out_sh", "out_st"))]
+
+
+ROPE_MAX = 8
+
+
+def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,
+         out=None):
+    """Rotary positions for x [B, heads, T, D] (or [heads, T, D]; any strides, D contiguous), or for a sequence of up
+    to 8 such tensors (q and k of a step) in one launch; float32 / bfloat16 / float16, one dtype per call.
+
+    positions: int32 / int64 device tensor [T] or [B, T].  freqs: float64 device tensor [rot / 2], radians per
+    position (rope_frequencies); channels from rot on pass unchanged.  Pairs are (i, i + rot/2), or (2i, 2i + 1) when
+    interleaved.  inverse=True turns back: with the same mscale the adjoint, the gradient's pass.
+    out: None (new contiguous tensors), or what x is, with the same shapes; x itself for in place.
+    Returns a tensor, or a list for a sequence."""
+    one = isinstance(x, torch.Tensor)
+    xs = [x] if one else list(x)
+    if not xs or len(xs) > ROPE_MAX:
+        raise ValueError(f"1 to {ROPE_MAX} tensors per call")
+    x0 = xs[0]
+    dev, dt = _rows(x0, "x").device, _dt(x0)
+    outs = [None] * len(xs) if out is None else [out] if one else list(out)
+    if len(outs) != len(xs):
+        raise ValueError("one output per tensor")
+    nd = x0.dim()
+    if nd not in (3, 4):
+        raise ValueError("x must be [B, heads, T, D] or [heads, T, D]")
+    B, T, D = x0.shape[0] if nd == 4 else 1, x0.shape[-2], x0.shape[-1]
+    _cuda(freqs, "freqs")
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or freqs.device != dev:
+        raise TypeError("freqs must be a 1-D float64 tensor on x's device")
+    rot = 2 * freqs.shape[0]
+    if rot > D:
+        raise ValueError("freqs holds more pairs than x has channels")
+    if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be an int32 or int64 CUDA tensor")
+    if positions.shape not in ((T,), (B, T)) or positions.device != dev:
+        raise ValueError("positions must be [T] or [B, T] on x's device")
+    ps = positions.stride()
+    descs = (_RopeTensor * len(xs))()
+    for j, (a, o) in enumerate(zip(xs, outs)):
+        _rows(a, "x")
+        if a.dim() != nd or a.shape[-2:] != (T, D) or (nd == 4 and a.shape[0] != B) or a.dtype != x0.dtype or a.device != dev:
+            raise ValueError("the tensors of a call share batch, length, head_dim, dtype and device")
+        if o is None:
+            o = outs[j] = torch.empty(a.shape, dtype=a.dtype, device=dev)
+        else:
+            _rows(o, "out")
+            if o.shape != a.shape or o.dtype != a.dtype or o.device != dev:
+                raise ValueError("out must have x's shape, dtype and device")
+            _no_shared_elements(o, "out")
+            if any(o.data_ptr() == outs[i].data_ptr() and o.numel() for i in range(j)):
+                raise ValueError("two outputs are the same tensor")
+            if not (o.data_ptr() == a.data_ptr() and o.stride() == a.stride()) and any(_overlap(o, b) for b in xs):
+                raise ValueError("out must be x itself or not overlap any x")
+        sx, so = a.stride(), o.stride()
+        descs[j] = _RopeTensor(a.data_ptr(), o.data_ptr(), a.shape[-3], sx[0] if nd == 4 else 0, sx[-3], sx[-2],
+                               so[0] if nd == 4 else 0, so[-3], so[-2])
+    _launch(dev, lib().nvfp4_rope, descs, len(xs), B, T, D, rot, int(bool(interleaved)), dt, positions.data_ptr(),
+            int(positions.dtype == torch.int64), ps[0] if len(ps) == 2 else 0, ps[-1], freqs.data_ptr(), float(mscale),
+            int(bool(inverse)))
+    return outs[0] if one else outs
+
+
+class _PagesArray(ctypes.Structure):
+    """nvfp4_pages_array (include/nvfp4.h)."""
+    _fields_ = [("base", _P), ("outer", _I64), ("stride", _I64), ("item", _I64), ("pages", _I64)]
+
+
+PAGES_MAX = 16
+
+
+def copy_pages(arrays, src, dst) -> None:
+    """Copies page src[j] to page dst[j] in every array, in one launch per 1024 pairs.  arrays: up to 16 pairs
+    (tensor, dim): a contiguous CUDA tensor of any dtype whose dimension `dim` counts pages.  src, dst: host
+    integers (sequences); all pairs move at once, so every dst is distinct and none of them is a src."""
+    arrays = list(arrays)
+    if len(arrays) > PAGES_MAX:
+        raise ValueError(f"at most {PAGES_MAX} arrays per call")
+    if len(src) != len(dst):
+        raise ValueError("src and dst differ in length")
+    if not arrays or not len(src):
+        return
+    descs = (_PagesArray * len(arrays))()
+    dev = arrays[0][0].device
+    for j, (t, dim) in enumerate(arrays):
+        _cuda(t, f"array {j}")
+        if t.device != dev:
+            raise ValueError(f"array {j} is on {t.device}, the call runs on {dev}")
+        if not -t.dim() <= dim < t.dim():
+            raise ValueError(f"array {j} has no dimension {dim}")
+        dim %= t.dim()
+        outer, pages = math.prod(t.shape[:dim]), t.shape[dim]
+        item = math.prod(t.shape[dim + 1:]) * t.element_size()
+        descs[j] = _PagesArray(t.data_ptr(), outer, pages * item, item, pages)
+    if any(a[0].numel() and b[0].numel() and _overlap(a[0], b[0]) for i, a in enumerate(arrays) for b in arrays[:i]):
+        raise ValueError("two arrays overlap")
+    s, d = (array.array("i", list(v)) for v in (src, dst))
+    _launch(dev, lib().nvfp4_copy_pages, descs, len(arrays), s.buffer_info()[0], d.buffer_info()[0], len(s))

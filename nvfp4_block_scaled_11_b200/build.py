@@ -2,12 +2,13 @@
 
     python -m nvfp4_block_scaled_11_b200.build [--force] [-v]
 
-Two translation units, compiled to objects under _build/ and linked into one shared library with the
+Three translation units, compiled to objects under _build/ and linked into one shared library with the
 CUDA runtime linked statically:
 
 * csrc/nvfp4_api.cu -- quantize / dequantize / Hadamard / KV kernels and the C ABI, compiled with
   -fmad=false so that no multiply-add is contracted where the definition rounds twice (fused
   operations are written out explicitly where they are wanted);
+* csrc/decode_api.cu -- attention over the K/V cache, rotary positions and page copies;
 * csrc/gemm_nvfp4.cu -- the tensor-core NVFP4 product, built on the CUTLASS / CuTe headers (the
   include tree shipped with the flashinfer package, or NVFP4_CUTLASS_INCLUDE).
 
@@ -47,11 +48,15 @@ def cutlass_include() -> list[str]:
 
 def _units():
     hdr = os.path.join(INC, "nvfp4.h")
-    cuh = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".cuh")]
+    decode_only = {"kv_attention.cuh", "pages.cuh", "rope.cuh"}
+    cuh = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".cuh") and f not in decode_only]
+    decode_cuh = [os.path.join(CSRC, f) for f in ("api_util.cuh", "device.cuh", *sorted(decode_only))]
     api = os.path.join(CSRC, "nvfp4_api.cu")
+    decode = os.path.join(CSRC, "decode_api.cu")
     gemm = os.path.join(CSRC, "gemm_nvfp4.cu")
     return [
         (api, [api, hdr, *cuh], ["-fmad=false"]),
+        (decode, [decode, hdr, *decode_cuh], []),
         (gemm, [gemm, hdr], ["--expt-relaxed-constexpr", "-diag-suppress", "20012", *cutlass_include()]),
     ]
 

@@ -1,0 +1,342 @@
+// decode_api.cu -- C ABI of the decode path (include/nvfp4.h): attention over the K/V cache, rotary
+// positions, page copies.  Argument validation and kernel launches.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <stdlib.h>
+#include <string.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/nvfp4.h"
+#include "api_util.cuh"
+#include "kv_attention.cuh"
+#include "pages.cuh"
+#include "rope.cuh"
+
+using namespace nvfp4;
+
+namespace {
+
+// Raises a kernel's shared-memory limit once per device.
+template <auto* kernel>
+int raise_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return NVFP4_ERR_CUDA;
+  if (done.load(std::memory_order_acquire) >> dev & 1u) return NVFP4_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_ERR_CUDA;
+  }
+  done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  return NVFP4_OK;
+}
+
+template <int D, int NT, bool QBF>
+int launch_kv_attention(const KvAttnParams& p, unsigned grid, unsigned rows, cudaStream_t s) {
+  constexpr int smem = KaSmem<D, NT>::kBytes;
+  if (int rc = raise_smem<kv_attn_kernel<D, NT, QBF>>(smem)) return rc;
+  kv_attn_kernel<D, NT, QBF><<<grid, kKaWarps * 32, smem, s>>>(p);
+  if (int rc = last_error()) return rc;
+  if (p.nch > 1) {
+    // launched while the first kernel drains; it waits for that kernel's results itself
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(rows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, QBF>, p) != cudaSuccess) {
+      cudaGetLastError();
+      return NVFP4_ERR_CUDA;
+    }
+  }
+  return last_error();
+}
+
+template <int D>
+int launch_kv_attention_d(const KvAttnParams& p, bool bf, int nt, unsigned grid, unsigned rows, cudaStream_t s) {
+  if (nt == 1) return bf ? launch_kv_attention<D, 1, true>(p, grid, rows, s) : launch_kv_attention<D, 1, false>(p, grid, rows, s);
+  return bf ? launch_kv_attention<D, 2, true>(p, grid, rows, s) : launch_kv_attention<D, 2, false>(p, grid, rows, s);
+}
+
+// Query rows of a CTA in units of 8: one K/V head's rows fit 8 for most decode steps; more rows share the
+// expansion of the codes in tiles of 16.
+int ka_row_units(int64_t rows) { return rows <= 8 ? 1 : 2; }
+
+// One side of the cache: pointers and layout into the kernel's form.
+int ka_side(const nvfp4_kv_store& c, const nvfp4_kv_attention_desc& d, int64_t mid_rows, KvSide& o) {
+  if ((c.rotate != 0 && c.rotate != 1) || (c.scale_layout != 0 && c.scale_layout != 1) ||
+      (c.gscale_stride != 0 && c.gscale_stride != 1))
+    return NVFP4_ERR_ARG;
+  if ((d.sink_rows > 0 && c.sink == nullptr) || (d.window_rows > 0 && c.window == nullptr) ||
+      (mid_rows > 0 && (c.codes == nullptr || c.scales == nullptr || c.gscale == nullptr)))
+    return NVFP4_ERR_ARG;
+  if (!aligned(c.sink, 16) || !aligned(c.window, 16) || !aligned(c.codes, 16) || !aligned(c.scales, 4) || !aligned(c.gscale, 4))
+    return NVFP4_ERR_ALIGN;
+  o.sink = static_cast<const char*>(c.sink);
+  o.window = static_cast<const char*>(c.window);
+  o.codes = c.codes;
+  o.scales = c.scales;
+  o.gscale = c.gscale;
+  o.gstride = c.gscale_stride;
+  o.rotate = c.rotate;
+  o.tile = c.scale_layout;
+  o.mat_bytes = (d.page_rows + 127) / 128 * 128 * (d.D / 64) * 4;
+  o.vec16 = !c.scale_layout && d.page_rows * (d.D / 16) % 16 == 0 && aligned(c.scales, 16);
+  return NVFP4_OK;
+}
+
+constexpr int64_t kMaxInt = INT_MAX;
+
+}  // namespace
+
+extern "C" {
+
+int nvfp4_kv_attention_splits(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t max_mid, int* splits) {
+  if (splits == nullptr) return NVFP4_ERR_ARG;
+  if (B < 0 || Hkv < 0 || rows < 0 || max_mid < 0 || max_mid > kMaxInt || (D != 64 && D != 128 && D != 256) ||
+      checked_prod({B, Hkv, rows, D, kKaMaxSplits, 4}) < 0)
+    return NVFP4_ERR_SIZE;
+  *splits = 1;
+  const int nt = ka_row_units(rows);
+  const int64_t base = B * Hkv * ((rows + 8 * nt - 1) / (8 * nt)), tiles = (max_mid + kKaTile - 1) / kKaTile;
+  if (base == 0 || tiles <= kKaMinTiles) return NVFP4_OK;
+  const int64_t slots = (int64_t)sm_count() * (D == 256 ? 2 : nt == 2 ? 3 : 4);
+  const int64_t want = std::max<int64_t>(1, (2 * slots + base - 1) / base);
+  *splits = (int)std::min<int64_t>({want, (tiles + kKaMinTiles - 1) / kKaMinTiles, (int64_t)kKaMaxSplits});
+  return NVFP4_OK;
+}
+
+size_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int splits) {
+  if (splits <= 1 || splits > kKaMaxSplits || B < 0 || Hkv < 0 || rows < 0 || D <= 0 ||
+      checked_prod({B, Hkv, rows, D + 2, splits, 4}) < 0)
+    return 0;
+  return (size_t)(B * Hkv * rows * (D + 2) * splits * 4);
+}
+
+int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (desc == nullptr || splits < 1 || splits > kKaMaxSplits) return NVFP4_ERR_ARG;
+  const nvfp4_kv_attention_desc& d = *desc;
+  if ((d.dtype != NVFP4_BF16 && d.dtype != NVFP4_F16) || (d.causal != 0 && d.causal != 1)) return NVFP4_ERR_ARG;
+  if (d.D != 64 && d.D != 128 && d.D != 256) return NVFP4_ERR_SIZE;
+  if (d.B < 0 || d.Hq < 0 || d.Hkv < 0 || d.Tq < 0 || d.slots < 0 || d.sink_rows < 0 || d.window_rows < 0 || d.pages < 0 ||
+      d.page_rows < 0 || d.table_cols < 0)
+    return NVFP4_ERR_SIZE;
+  if (d.B > kMaxInt || d.Hq > kMaxInt || d.Tq > kMaxInt || d.slots > kMaxInt || d.sink_rows > kMaxInt / 4 ||
+      d.window_rows > kMaxInt / 4 || d.pages > kMaxInt || d.page_rows > kMaxInt)
+    return NVFP4_ERR_SIZE;
+  if (d.B == 0 || d.Hq == 0 || d.Tq == 0) return NVFP4_OK;
+  if (d.Hkv == 0 || d.Hq % d.Hkv != 0) return NVFP4_ERR_SIZE;
+  if (d.slot == nullptr && d.B > d.slots) return NVFP4_ERR_SIZE;
+  int64_t mid_rows = d.page_rows;                      // a sequence's middle at most
+  if (d.table != nullptr) {
+    if (d.page_rows == 0 || d.page_rows % 16 != 0) return NVFP4_ERR_SIZE;
+    mid_rows = checked_prod({d.table_cols, d.page_rows});
+    if (mid_rows < 0 || mid_rows > kMaxInt || checked_prod({d.slots, d.table_cols, 4}) < 0) return NVFP4_ERR_SIZE;
+  } else if (d.pages < d.slots) {
+    return NVFP4_ERR_SIZE;                             // slot s is page s
+  }
+  if (checked_prod({d.slots, d.Hkv, d.sink_rows + d.window_rows, d.D, 2}) < 0 ||
+      checked_prod({d.pages, d.Hkv, (d.page_rows + 127) / 128 * 128, d.D}) < 0)
+    return NVFP4_ERR_SIZE;
+  if (d.lens == nullptr &&
+      (d.n_sink < 0 || d.n_sink > d.sink_rows || d.n_mid < 0 || d.n_mid > mid_rows || d.n_window < 0 ||
+       d.n_window > d.window_rows || d.head < 0 || d.head > std::max<int64_t>(d.window_rows - 1, 0)))
+    return NVFP4_ERR_ARG;
+  if (d.q == nullptr || d.out == nullptr) return NVFP4_ERR_ARG;
+  if (!aligned(d.q, 2) || !aligned(d.out, 2) || !aligned(d.lse, 4) || !aligned(d.slot, 4) || !aligned(d.table, 4) ||
+      !aligned(d.lens, 4) || !aligned(workspace, 16))
+    return NVFP4_ERR_ALIGN;
+  KvAttnParams p{};
+  if (int rc = ka_side(d.k, d, d.pages > 0 ? mid_rows : 0, p.k)) return rc;
+  if (int rc = ka_side(d.v, d, d.pages > 0 ? mid_rows : 0, p.v)) return rc;
+  const int64_t G = d.Hq / d.Hkv, R = checked_prod({G, d.Tq});
+  if (R < 0 || R > kMaxInt) return NVFP4_ERR_SIZE;
+  const int nt = ka_row_units(R);
+  const int64_t row_tiles = (R + 8 * nt - 1) / (8 * nt);
+  const int64_t grid = checked_prod({d.B, d.Hkv, row_tiles, splits}), rows = checked_prod({d.B, d.Hkv, R});
+  if (grid < 0 || grid > kMaxInt || rows < 0 || rows > kMaxInt || checked_prod({rows, d.D + 2, splits, 4}) < 0)
+    return NVFP4_ERR_SIZE;
+  if (splits > 1) {
+    if (workspace == nullptr) return NVFP4_ERR_ARG;
+    if (workspace_bytes < nvfp4_kv_attention_workspace_bytes(d.B, d.Hkv, R, d.D, splits)) return NVFP4_ERR_SIZE;
+  }
+  p.q = static_cast<const char*>(d.q);
+  p.out = static_cast<char*>(d.out);
+  p.lse = d.lse;
+  p.q_sb = d.q_sb, p.q_sh = d.q_sh, p.q_st = d.q_st;
+  p.o_sb = d.out_sb, p.o_sh = d.out_sh, p.o_st = d.out_st;
+  p.Hq = (int)d.Hq, p.Hkv = (int)d.Hkv, p.G = (int)G, p.Tq = (int)d.Tq, p.R = (int)R, p.row_tiles = (int)row_tiles;
+  p.sink_rows = (int)d.sink_rows, p.window_rows = (int)d.window_rows, p.page_rows = (int)d.page_rows;
+  p.page_shift = -1;
+  if (d.page_rows > 0 && (d.page_rows & (d.page_rows - 1)) == 0) p.page_shift = __builtin_ctzll((unsigned long long)d.page_rows);
+  p.slots = d.slots, p.pages = d.pages, p.cols = d.table_cols;
+  p.slot = d.slot, p.table = d.table, p.lens = d.lens;
+  p.host_lens[0] = d.n_sink, p.host_lens[1] = d.n_mid, p.host_lens[2] = d.head, p.host_lens[3] = d.n_window;
+  p.nch = splits;
+  p.causal = d.causal;
+  p.q_vec = aligned(d.q, 16) && d.q_sb % 8 == 0 && d.q_sh % 8 == 0 && d.q_st % 8 == 0;
+  p.scale_log2 = d.scale * 1.4426950408889634f;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + (splits > 1 ? rows * splits * d.D : 0));
+  const bool bf = d.dtype == NVFP4_BF16;
+  cudaStream_t s = S(stream);
+  if (d.D == 64) return launch_kv_attention_d<64>(p, bf, nt, (unsigned)grid, (unsigned)rows, s);
+  if (d.D == 128) return launch_kv_attention_d<128>(p, bf, nt, (unsigned)grid, (unsigned)rows, s);
+  return launch_kv_attention_d<256>(p, bf, nt, (unsigned)grid, (unsigned)rows, s);
+}
+
+int nvfp4_rope(const nvfp4_rope_tensor* tensors, int count, int64_t B, int64_t T, int64_t D, int64_t rot, int interleaved,
+               int dtype, const void* positions, int positions64, int64_t pos_sb, int64_t pos_st, const double* freqs,
+               float mscale, int inverse, void* stream) {
+  if (count < 0 || count > kRopeMaxTensors || (count > 0 && tensors == nullptr) || !dtype_ok(dtype) ||
+      (interleaved != 0 && interleaved != 1) || (positions64 != 0 && positions64 != 1) || (inverse != 0 && inverse != 1))
+    return NVFP4_ERR_ARG;
+  if (B < 0 || T < 0 || D < 0 || rot < 0 || rot > D || rot % 2 != 0 || rot / 2 > kRopeMaxPairs || D > kMaxInt ||
+      checked_prod({B, T}) < 0)
+    return NVFP4_ERR_SIZE;
+  RopeParams p{};
+  int64_t heads = 0;
+  const int es = esize(dtype), V = 16 / es;
+  bool vec = D % V == 0 && rot % V == 0 && (interleaved || (rot / 2) % V == 0);
+  for (int k = 0; k < count; ++k) {
+    const nvfp4_rope_tensor& a = tensors[k];
+    if (a.heads < 0 || a.heads > kMaxInt) return NVFP4_ERR_SIZE;
+    if (a.heads == 0 || B == 0 || T == 0 || D == 0) continue;
+    if (a.x == nullptr || a.out == nullptr) return NVFP4_ERR_ARG;
+    if (!aligned(a.x, es) || !aligned(a.out, es)) return NVFP4_ERR_ALIGN;
+    // in place only element by element: every element is written where it was read
+    if (a.x == a.out && (a.x_sb != a.out_sb || a.x_sh != a.out_sh || a.x_st != a.out_st)) return NVFP4_ERR_ARG;
+    vec = vec && aligned(a.x, 16) && aligned(a.out, 16) && a.x_sb % V == 0 && a.x_sh % V == 0 && a.x_st % V == 0 &&
+          a.out_sb % V == 0 && a.out_sh % V == 0 && a.out_st % V == 0;
+    p.a[p.count++] = RopeTensor{static_cast<const char*>(a.x), static_cast<char*>(a.out), (int)a.heads, a.x_sb, a.x_sh,
+                                a.x_st, a.out_sb, a.out_sh, a.out_st};
+    heads += a.heads;
+  }
+  if (p.count == 0) return NVFP4_OK;
+  if (positions == nullptr || (rot > 0 && freqs == nullptr)) return NVFP4_ERR_ARG;
+  if (!aligned(positions, positions64 ? 8 : 4) || !aligned(freqs, 8)) return NVFP4_ERR_ALIGN;
+  if (heads > kMaxInt / 4096) return NVFP4_ERR_SIZE;   // (token, head) rows of a CTA are counted in 32 bits
+  p.heads = (int)heads;
+  p.tokens = B * T;
+  p.T = T;
+  p.D = (int)D;
+  p.rot = (int)rot;
+  p.interleaved = interleaved;
+  p.pos64 = positions64;
+  p.pos = positions;
+  p.pos_b = pos_sb;
+  p.pos_t = pos_st;
+  p.freqs = freqs;
+  p.mscale = mscale;
+  p.sign = inverse ? -1.0f : 1.0f;
+  const int v = vec ? V : (interleaved ? 2 : 1);
+  // odd D - rot with single pairs: pieces of two channels would miss the last one
+  if (!vec && interleaved && (D - rot) % 2 != 0) return NVFP4_ERR_SIZE;
+  const int64_t half = rot / 2, pieces = (interleaved ? rot : half) / v + (D - rot) / v;
+  const int64_t per_pass = std::max<int64_t>(1, kRopeThreads / std::max<int64_t>(1, pieces));
+  const int sms = sm_count();
+  // tokens per CTA: as many as leave four CTAs per SM, up to 8 passes of its threads over (token, head) rows
+  int64_t tile = 1;
+  while (tile < 32 && 2 * tile * half <= kRopeSmemPairs && p.tokens / (2 * tile) >= 4 * sms && 2 * tile * heads <= 8 * per_pass)
+    tile *= 2;
+  p.tile = (int)tile;
+  const int64_t gx = (p.tokens + tile - 1) / tile;
+  if (gx > kMaxInt) return NVFP4_ERR_SIZE;
+  // few tokens (a decode step): the heads of a token are shared among CTAs until there are two per SM
+  const int64_t passes = (tile * heads + per_pass - 1) / per_pass;
+  const int64_t gy = gx >= 2 * sms ? 1 : std::max<int64_t>(1, std::min<int64_t>({passes, (2 * sms + gx - 1) / gx, 64}));
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  cudaStream_t s = S(stream);
+#define NVFP4_ROPE(DT)                                                              \
+  do {                                                                              \
+    if (interleaved) {                                                              \
+      if (vec) rope_kernel<DT, true, true><<<grid, kRopeThreads, 0, s>>>(p);        \
+      else rope_kernel<DT, true, false><<<grid, kRopeThreads, 0, s>>>(p);           \
+    } else {                                                                        \
+      if (vec) rope_kernel<DT, false, true><<<grid, kRopeThreads, 0, s>>>(p);       \
+      else rope_kernel<DT, false, false><<<grid, kRopeThreads, 0, s>>>(p);          \
+    }                                                                               \
+  } while (0)
+  if (dtype == NVFP4_F32) NVFP4_ROPE(DT_F32);
+  else if (dtype == NVFP4_BF16) NVFP4_ROPE(DT_BF16);
+  else NVFP4_ROPE(DT_F16);
+#undef NVFP4_ROPE
+  return last_error();
+}
+
+int nvfp4_copy_pages(const nvfp4_pages_array* arrays, int count, const int32_t* src, const int32_t* dst, int64_t n,
+                     void* stream) {
+  if (count < 0 || count > kPagesMaxArrays || (count > 0 && arrays == nullptr)) return NVFP4_ERR_ARG;
+  if (n < 0 || n > kMaxInt) return NVFP4_ERR_SIZE;
+  if (n > 0 && (src == nullptr || dst == nullptr)) return NVFP4_ERR_ARG;
+  int64_t pages = kMaxInt;                             // pages that every array has
+  for (int k = 0; k < count; ++k) {
+    const nvfp4_pages_array& a = arrays[k];
+    if (a.outer < 0 || a.outer > kMaxInt || a.item < 0 || a.pages < 0 || a.stride < 0) return NVFP4_ERR_SIZE;
+    if (checked_prod({a.pages, a.item}) < 0 || checked_prod({a.outer, a.stride}) < 0) return NVFP4_ERR_SIZE;
+    if (a.outer > 1 && a.stride < a.pages * a.item) return NVFP4_ERR_SIZE;   // pieces of pages must not overlap
+    if (a.outer > 0 && a.item > 0 && a.pages > 0 && a.base == nullptr) return NVFP4_ERR_ARG;
+    pages = std::min(pages, a.pages);
+  }
+  if (n == 0 || count == 0) return NVFP4_OK;
+  for (int64_t i = 0; i < n; ++i)
+    if (src[i] < 0 || src[i] >= pages || dst[i] < 0 || dst[i] >= pages) return NVFP4_ERR_ARG;
+  // every destination once and none a source: all pairs move at the same time
+  int32_t* v = static_cast<int32_t*>(malloc((size_t)n * 2 * sizeof(int32_t)));
+  if (v == nullptr) return NVFP4_ERR_SIZE;
+  memcpy(v, dst, (size_t)n * sizeof(int32_t));
+  memcpy(v + n, src, (size_t)n * sizeof(int32_t));
+  std::sort(v, v + n);
+  std::sort(v + n, v + 2 * n);
+  bool clash = false;
+  for (int64_t i = 0, j = 0; i < n; ++i) {
+    clash |= i > 0 && v[i] == v[i - 1];
+    while (j < n && v[n + j] < v[i]) ++j;
+    clash |= j < n && v[n + j] == v[i];
+  }
+  free(v);
+  if (clash) return NVFP4_ERR_ARG;
+  PagesParams p{};
+  int64_t per_pair = 0;                                // CTAs for one page of every array
+  for (int k = 0; k < count; ++k) {
+    const nvfp4_pages_array& a = arrays[k];
+    if (a.outer == 0 || a.item == 0) continue;
+    PagesArray& o = p.a[p.count++];
+    o.base = static_cast<char*>(a.base);
+    o.stride = a.outer > 1 ? a.stride : 0;
+    o.item = a.item;
+    o.outer = (int)a.outer;
+    o.parts = (a.item + kPagesPiece - 1) / kPagesPiece;
+    const uint64_t bits = (uint64_t)reinterpret_cast<uintptr_t>(a.base) | (uint64_t)o.stride | (uint64_t)a.item;
+    o.width = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+    const int64_t ctas = checked_prod({a.outer, o.parts});
+    if (ctas < 0 || ctas > kMaxInt - per_pair) return NVFP4_ERR_SIZE;
+    per_pair += ctas;
+  }
+  if (p.count == 0) return NVFP4_OK;
+  const int64_t step = std::min<int64_t>(kPagesPairs, kMaxInt / per_pair);
+  for (int64_t i = 0; i < n; i += step) {
+    p.n = (int)std::min(step, n - i);
+    memcpy(p.src, src + i, (size_t)p.n * sizeof(int32_t));
+    memcpy(p.dst, dst + i, (size_t)p.n * sizeof(int32_t));
+    int64_t total = 0;
+    for (int k = 0; k < p.count; ++k) {
+      p.start[k] = total;
+      total += (int64_t)p.a[k].outer * p.a[k].parts * p.n;
+    }
+    p.start[p.count] = total;
+    copy_pages_kernel<<<(unsigned)total, kPagesThreads, 0, S(stream)>>>(p);
+    if (int rc = last_error()) return rc;
+  }
+  return NVFP4_OK;
+}
+
+}  // extern "C"

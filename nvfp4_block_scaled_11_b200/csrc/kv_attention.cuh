@@ -1,0 +1,933 @@
+// kv_attention.cuh -- attention of new tokens over the mixed-precision K/V cache (decode).
+//
+// "Search your block floating-point scales!" (gist.science summary of arXiv 2605.12464),
+// ScaleSearchAttention > attention-sink-aware mixed-precision caching: the cache that nvfp4_kv_append
+// fills is read where it lies.  Per sequence the tokens are, in order,
+//   sink (BF16) | middle (NVFP4, rotated by H16/4 along head_dim when `rotate`) | window (BF16 ring).
+// For query token i of Tq (the newest tokens of the sequence, L tokens in all) and key t at position t:
+//   s_t = scale q . k_t for t <= L - Tq + i (causal) or every t;  O = sum softmax(s)_t v_t.
+// In the middle k_t = H16/4 (code e4m3 g_k), so q . k_t = (H16/4 q) . (code e4m3) g_k: the query is rotated
+// once and the keys never; O's middle part is accumulated in rotated space and turned back once.
+//
+// One pass over the tokens with a running maximum and sum (kv_attn_kernel), a CTA per (sequence, K/V head,
+// tile of query rows, range of the middle); ranges are joined by kv_attn_combine_kernel.  The bytes of
+// the cache bound it (2 (D/2 + D/16) per token and K/V head), so the design keeps copies in flight and the
+// instructions per byte low:
+// * every warp owns its tiles of 32 tokens and its own ring of shared-memory stages filled by cp.async: no
+//   CTA-wide barrier inside the loop, rows behind the end arrive as zeros;
+// * code * e4m3 has at most 6 significant bits and lies in [2^-10, 2688], so the products' operands are exact
+//   in FP16: one convert and one multiply give two elements, and m16n8k16 products with FP32 accumulators
+//   take keys (or values' channels) as the 16 rows and query rows as the 8 columns.  tcgen05 would want
+//   128 rows of expanded tiles in shared memory for 8 useful columns: the expansion would cross shared
+//   memory once more and the accumulators TMEM, for a product that is not what bounds the pass;
+// * the rotated query is split into two FP16 terms (22 bits after a power-of-two row scale), so scores
+//   keep FP32 accuracy; the numerators are rounded to FP16 once, scaled by 2^15 (full precision down to
+//   2^-29 of the row's maximum, 2^-12 relative error each; sums are taken in FP32 before that rounding);
+// * S^T = K Q^T leaves (token, query) fragments; movmatrix turns the FP16 numerators into the second
+//   product's operand; V is packed along channels, so pairs of tokens are interleaved nibble by nibble
+//   (two logic operations per 8 codes and token) before the converts.
+#pragma once
+
+#include <float.h>
+#include <limits.h>
+#include <math.h>
+
+#include "device.cuh"
+
+namespace nvfp4 {
+
+constexpr int kKaWarps = 4;            // warps per CTA, each with its own tiles
+constexpr int kKaTile = 32;            // middle tokens per tile
+constexpr int kKaMinTiles = 8;         // least tiles per range: shorter ones cost more in joining than they win
+constexpr int kKaMaxSplits = 128;
+constexpr float kKaPShift = 15.0f;     // numerators of the middle are scaled by 2^15 before FP16
+
+struct KvSide {
+  const char* sink;        // BF16 [slots, Hkv, sink_rows, D]
+  const char* window;      // BF16 ring [slots, Hkv, window_rows, D]
+  const uint8_t* codes;    // [pages, Hkv, page_rows, D/2]
+  const uint8_t* scales;   // [pages, Hkv, page_rows, D/16] or tile layout
+  const float* gscale;     // one, or one per slot
+  int64_t gstride;         // 0 or 1
+  int64_t mat_bytes;       // tile layout: bytes of one [page_rows, D] matrix
+  int rotate, tile, vec16; // vec16: scale rows may be copied 16 bytes at a time
+};
+
+struct KvAttnParams {
+  const char* q;
+  char* out;
+  float* lse;              // [B, Hq, Tq] or null
+  int64_t q_sb, q_sh, q_st, o_sb, o_sh, o_st;   // strides in elements
+  KvSide k, v;
+  int Hq, Hkv, G, Tq, R, row_tiles;             // R = G Tq rows per K/V head, row r = token r / G, head r % G
+  int sink_rows, window_rows, page_rows, page_shift;
+  int64_t slots, pages, cols;
+  const int32_t* slot;     // [B] or null: sequence b is slot b
+  const int32_t* table;    // [slots, cols] or null: slot s is page s
+  const int32_t* lens;     // [slots, 4] (n_sink, n_mid, head, n_window) or null: host_lens for every slot
+  int host_lens[4];
+  int nch, causal, q_vec;
+  float scale_log2;        // scale * log2(e)
+  float* ws_o;             // [B Hkv R, nch, D]
+  float2* ws_ml;           // [B Hkv R, nch] maxima (base 2) and sums
+};
+
+template <int D>
+struct KaShape {
+  static constexpr int kCodeRow = D / 2, kScaleRow = D / 16;
+  static constexpr int kKC = 0, kVC = kKaTile * kCodeRow, kKS = 2 * kKaTile * kCodeRow, kVS = kKS + kKaTile * kScaleRow;
+  static constexpr int kStageBytes = 2 * kKaTile * (kCodeRow + kScaleRow);
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kRing = kKaWarps * kStages * kStageBytes;
+};
+template <int D, int NT>
+struct KaSmem {
+  static constexpr int kAccRow = D + 4;                                   // floats, padded
+  static constexpr int kAcc = kKaWarps * 8 * NT * kAccRow * 4;            // the join of the warps reuses the ring
+  static constexpr int kRing = KaShape<D>::kRing > kAcc ? KaShape<D>::kRing : kAcc;
+  static constexpr int kQ = NT * (D / 16) * 32 * 16;                      // one query operand (hi and lo)
+  static constexpr int kStat = kKaWarps * 8 * NT * 8;
+  static constexpr int kBytes = kRing + 2 * kQ + kStat + 8 * NT * 8 + kKaWarps * KaShape<D>::kStages * 4;
+};
+
+// ---- small instruction wrappers ----
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // the rest is zero-filled
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (BF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// the four bytes of w (two E2M1 codes each) as f16x2
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b; cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d; }"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// two E4M3 bytes (low, high) as f16x2
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b2) {
+  uint32_t r;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(b2));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// (lo, hi) as two f16x2 terms: the rounded values and what they leave
+__device__ __forceinline__ void split_f16(float lo, float hi, uint32_t& a, uint32_t& b) {
+  a = pack_f16(lo, hi);
+  b = pack_f16(__fsub_rn(lo, f16lo(a)), __fsub_rn(hi, f16hi(a)));
+}
+// (lo, hi) as two bf16x2 terms of the same sign, neither of them zero unless the value is: a factor times an
+// infinite element of K or V then stays that infinity (a zero term would make it NaN).  The first term is the
+// value cut to 8 bits, the second the rest rounded to 8 (relative error 2^-16); without a rest both are halves.
+__device__ __forceinline__ void split_bf16(float lo, float hi, uint32_t& a, uint32_t& b) {
+  float h0 = __uint_as_float(__float_as_uint(lo) & 0xFFFF0000u), h1 = __uint_as_float(__float_as_uint(hi) & 0xFFFF0000u);
+  float r0 = __fsub_rn(lo, h0), r1 = __fsub_rn(hi, h1);
+  if (r0 == 0.0f) h0 = r0 = 0.5f * lo;
+  if (r1 == 0.0f) h1 = r1 = 0.5f * hi;
+  a = pack_bf16(h0, h1);
+  b = pack_bf16(r0, r1);
+}
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// The lengths of the sequence of batch row b, bounded by the buffers (an unknown slot is an empty sequence).
+struct KaSeq {
+  int s, ns, nm, head, nw;
+  int64_t len;
+};
+__device__ __forceinline__ KaSeq ka_sequence(const KvAttnParams& p, int b) {
+  KaSeq q;
+  const int64_t s = p.slot ? p.slot[b] : b;
+  const bool ok = s >= 0 && s < p.slots;
+  q.s = ok ? (int)s : 0;
+  int n[4];
+  if (p.lens) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n[k] = p.lens[4 * (int64_t)q.s + k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n[k] = p.host_lens[k];
+  }
+  const int64_t most = p.table ? p.cols * p.page_rows : p.page_rows;
+  q.ns = ok ? min(max(n[0], 0), p.sink_rows) : 0;
+  q.nm = ok ? (int)min((int64_t)max(n[1], 0), most) : 0;
+  q.nw = ok ? min(max(n[3], 0), p.window_rows) : 0;
+  q.head = p.window_rows > 0 ? (int)((uint32_t)n[2] % (uint32_t)p.window_rows) : 0;
+  q.len = (int64_t)q.ns + q.nm + q.nw;
+  return q;
+}
+// Tiles per range and the ranges that hold any (at least one) of a middle of nm tokens.
+__device__ __forceinline__ void ka_ranges(int nm, int nch, int& per, int& active) {
+  const int tiles = (nm + kKaTile - 1) / kKaTile;
+  per = max((tiles + nch - 1) / nch, kKaMinTiles);
+  active = max((tiles + per - 1) / per, 1);
+}
+
+template <bool BF>
+__device__ __forceinline__ void ka_store(char* out, int64_t i, float x) {
+  if constexpr (BF) reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(x);
+  else reinterpret_cast<__half*>(out)[i] = __float2half_rn(x);
+}
+
+// D: head_dim; NT: query rows / 8 of a CTA; QBF: q and out are BF16 (else FP16).
+template <int D, int NT, bool QBF>
+__global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
+  using Sh = KaShape<D>;
+  using Sm = KaSmem<D, NT>;
+  constexpr int ST = Sh::kStages, NS = D / 16 /* k16 steps */, NO = D / 16 /* m16 tiles of channels */;
+  constexpr int KW = D >= 128 ? 4 : 2, KCH = D == 256 ? 2 : 1;      // code words per key chunk, chunks per thread
+  constexpr int VW = D / 64;                                         // code words of V per thread and token
+  constexpr int VB = D == 256 ? 2 : 1;                               // scale blocks of V per thread and token
+  constexpr int ROWS = 8 * NT;
+  extern __shared__ __align__(128) unsigned char smem[];
+  uint4* qf = reinterpret_cast<uint4*>(smem + Sm::kRing);            // rotated query, FP16 hi / lo, fragment order
+  uint4* qe = reinterpret_cast<uint4*>(smem + Sm::kRing + Sm::kQ);   // query as given, BF16 hi / lo
+  float2* stat = reinterpret_cast<float2*>(smem + Sm::kRing + 2 * Sm::kQ);
+  float* rowfac = reinterpret_cast<float*>(smem + Sm::kRing + 2 * Sm::kQ + Sm::kStat);
+  int* limit = reinterpret_cast<int*>(rowfac + ROWS);
+  uint32_t* vms = reinterpret_cast<uint32_t*>(limit + ROWS);         // [warp][stage]: the tile's tokens that exist
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
+  int x = blockIdx.x;
+  const int row_tile = x % p.row_tiles;
+  x /= p.row_tiles;
+  const int ch = x % p.nch;
+  x /= p.nch;
+  const int kvh = x % p.Hkv, b = x / p.Hkv;
+  const KaSeq sq = ka_sequence(p, b);
+  int per, active;
+  ka_ranges(sq.nm, p.nch, per, active);
+  if (ch >= active) return;
+  const int tiles = (sq.nm + kKaTile - 1) / kKaTile;
+  const int t_first = ch * per + w, t_end = min(tiles, (ch + 1) * per);
+  const int n_my = t_first < t_end ? (t_end - t_first + kKaWarps - 1) / kKaWarps : 0;
+
+  // ---- the warp's ring: tile i of this warp goes to stage i % ST ----
+  unsigned char* ring = smem + w * ST * Sh::kStageBytes;
+  const uint32_t ring_u = smem_u32(ring);
+  auto page_of = [&](int tok) -> int {          // the page holding middle token tok, -1: none
+    if (tok >= sq.nm) return -1;
+    if (!p.table) return sq.s;
+    const int c = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_rows;
+    const int pg = __ldg(p.table + (int64_t)sq.s * p.cols + c);
+    return pg >= 0 && pg < p.pages ? pg : -1;
+  };
+  auto row_in_page = [&](int tok) -> int {
+    if (!p.table) return tok;
+    return p.page_shift >= 0 ? tok & (p.page_rows - 1) : tok % p.page_rows;
+  };
+  auto issue = [&](int i, int pg0, int pg1) {
+    const int tok = (t_first + i * kKaWarps) * kKaTile, st = i % ST;
+    const uint32_t dst = ring_u + st * Sh::kStageBytes;
+    const int pg[2] = {pg0, pg1};
+    int64_t mat[2];
+    int r0[2];
+    uint32_t vm = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tk = tok + 16 * h, left = sq.nm - tk;
+      r0[h] = pg[h] >= 0 ? row_in_page(tk) : 0;
+      mat[h] = (int64_t)max(pg[h], 0) * p.Hkv + kvh;
+      if (pg[h] >= 0 && left > 0) vm |= (left >= 16 ? 0xFFFFu : (1u << left) - 1u) << (16 * h);
+    }
+    if (lane == 0) vms[w * ST + st] = vm;
+    constexpr int CPR = Sh::kCodeRow / 16, ITS = kKaTile * CPR / 32;   // 16-byte pieces per row, instructions
+#pragma unroll
+    for (int it = 0; it < ITS; ++it) {
+      constexpr int HALF = ITS / 2;
+      const int h = it / HALF, row = it * (32 / CPR) + lane / CPR;
+      const int ok = (vm >> row) & 1u;
+      const int64_t off = ok ? (mat[h] * p.page_rows + r0[h]) * Sh::kCodeRow + (it % HALF) * 512 + lane * 16 : 0;
+      const uint32_t at = (uint32_t)(it * 512 + lane * 16);
+      // keys are read as rows r and r + 4 together, values as rows r .. r + 3: each order gets its own
+      // exchange of 64- (32-) byte halves so that both read without bank conflicts
+      const uint32_t ka = at ^ (((uint32_t)row >> 2 & 1u) << 6);
+      const uint32_t va = D == 128 ? at ^ (((uint32_t)row >> 1 & 1u) << 5) : D == 256 ? at ^ (((uint32_t)row & 3u) << 5) : at;
+      cp_async16(dst + Sh::kKC + ka, p.k.codes + off, ok ? 16 : 0);
+      cp_async16(dst + Sh::kVC + va, p.v.codes + off, ok ? 16 : 0);
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const KvSide& s = side ? p.v : p.k;
+      const uint32_t sd = dst + (side ? Sh::kVS : Sh::kKS);
+      if (s.vec16) {
+        constexpr int RPP = 16 / Sh::kScaleRow, NP = kKaTile / RPP;    // rows per 16 bytes, pieces per tile
+        if (lane < NP) {
+          const int row = lane * RPP, h = row >> 4;
+          const int n = __popc((vm >> row) & ((1u << RPP) - 1u));
+          const int64_t off = n ? (mat[h] * p.page_rows + r0[h] + (row & 15)) * Sh::kScaleRow : 0;
+          cp_async16(sd + row * Sh::kScaleRow, s.scales + off, n * Sh::kScaleRow);
+        }
+      } else {
+        const int h = lane >> 4, ok = (vm >> lane) & 1u, r = r0[h] + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          int64_t off = 0;
+          if (ok)
+            off = s.tile ? mat[h] * s.mat_bytes + ((int64_t)(r >> 7) * (D / 64) + j) * 512 + 16 * (r & 31) + 4 * (r >> 5 & 3)
+                         : (mat[h] * p.page_rows + r) * Sh::kScaleRow + 4 * j;
+          cp_async4(sd + lane * Sh::kScaleRow + 4 * j, s.scales + off, ok ? 4 : 0);
+        }
+      }
+    }
+  };
+  int next[2];                                  // pages of the tile that is issued next
+  auto look_up = [&](int i) {
+    const int tok = (t_first + i * kKaWarps) * kKaTile;
+    next[0] = i < n_my ? page_of(tok) : -1;
+    next[1] = i < n_my ? page_of(tok + 16) : -1;
+  };
+  look_up(0);
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) {
+    const int a = next[0], c = next[1];
+    look_up(i + 1);
+    if (i < n_my) issue(i, a, c);
+    cp_async_commit();
+  }
+
+  // ---- the query rows: 16-channel blocks, rotated, scaled by a power of two per row, in fragment order ----
+  constexpr int BPR = D / 16;                   // blocks per row, handled by adjacent lanes
+#pragma unroll
+  for (int u0 = 0; u0 < ROWS * BPR; u0 += kKaWarps * 32) {
+    const int u = u0 + tid;
+    if (ROWS * BPR % (kKaWarps * 32) != 0 && u >= ROWS * BPR) break;   // whole warps leave (ROWS * BPR is a multiple of 32)
+    const int row = u / BPR, blk = u % BPR, r = row_tile * ROWS + row;
+    float a[16];
+    if (r < p.R) {
+      const int i = r / p.G, hq = kvh * p.G + r % p.G;
+      const int64_t at = b * p.q_sb + hq * p.q_sh + i * p.q_st + blk * 16;
+      uint32_t wd[8];
+      if (p.q_vec) {
+        ld_v4(p.q + at * 2, wd);
+        ld_v4(p.q + at * 2 + 16, wd + 4);
+      } else {
+        const unsigned short* s = reinterpret_cast<const unsigned short*>(p.q) + at;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) wd[k] = s[2 * k] | (uint32_t)s[2 * k + 1] << 16;
+      }
+      widen_words<QBF ? DT_BF16 : DT_F16>(wd, a, 8);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) a[k] = 0.0f;
+    }
+    // channel c of the row sits in key chunk c / CD, read by thread t of the fragment; 4 channels per step
+    constexpr int CD = D >= 128 ? 32 : 16;
+    const int c0 = blk * 16, chunk = c0 / CD, ft = chunk & 3, j0 = (chunk >> 2) * 8 + (c0 % CD) / 4;
+    const int fl = (row & 7) * 4 + ft, nt = row >> 3;
+    uint4* eo = qe + (nt * NS + j0) * 32 + fl;
+    uint4* fo = qf + (nt * NS + j0) * 32 + fl;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 v;
+      if constexpr (QBF) {
+        v = make_uint4(pack_bf16(a[4 * j], a[4 * j + 1]), pack_bf16(a[4 * j + 2], a[4 * j + 3]), 0u, 0u);
+      } else {
+        split_bf16(a[4 * j], a[4 * j + 1], v.x, v.z);
+        split_bf16(a[4 * j + 2], a[4 * j + 3], v.y, v.w);
+      }
+      eo[j * 32] = v;
+    }
+    if (p.k.rotate) fwht16(a);
+    float mx = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(a[k]));
+#pragma unroll
+    for (int o = BPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    int e = (int)(__float_as_uint(mx) >> 23) - 127;                  // floor(log2), exact for normal values
+    e = mx > 0.0f && mx <= FLT_MAX ? max(-100, min(100, e)) : 0;
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 v;
+      split_f16(a[4 * j] * down, a[4 * j + 1] * down, v.x, v.z);
+      split_f16(a[4 * j + 2] * down, a[4 * j + 3] * down, v.y, v.w);
+      fo[j * 32] = v;
+    }
+    if (blk == 0) {
+      rowfac[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+      // positions this row sees: all before the limit (rows past R restrict nothing and are not written)
+      int64_t lim = sq.len;
+      if (p.causal && r < p.R) lim = max(sq.len - p.Tq + r / p.G + 1, (int64_t)0);
+      limit[row] = (int)min(lim, (int64_t)INT_MAX);
+    }
+  }
+  __syncthreads();
+
+  float O[NO][NT][4], m[NT][2], l[NT][2], fac[NT][2];
+  int lim[NT][2];
+  int lim_min = INT_MAX;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      m[n][c] = -INFINITY;
+      l[n][c] = 0.0f;
+      lim[n][c] = limit[8 * n + 2 * t + c];
+      lim_min = min(lim_min, lim[n][c]);
+      fac[n][c] = rowfac[8 * n + 2 * t + c];
+    }
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) O[i][n][c] = 0.0f;
+  }
+  lim_min = min(lim_min, __shfl_xor_sync(0xFFFFFFFFu, lim_min, 1));
+  lim_min = min(lim_min, __shfl_xor_sync(0xFFFFFFFFu, lim_min, 2));
+  const int perm = (g >> 1) + 4 * (g & 1);      // the token of fragment row g (row g + 8: + 8)
+
+  // running maximum: raise m to the tile's maxima, rescaling what was summed under the old ones
+  auto raise = [&](float (&mx)[NT][2]) {
+    bool up = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xFFFFFFFFu, mx[n][c], o));
+        up |= mx[n][c] > m[n][c];
+      }
+    if (!__any_sync(0xFFFFFFFFu, up)) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float mn = fmaxf(m[n][c], mx[n][c]);
+        const float al = ex2(m[n][c] - finite_or_zero(mn));
+        m[n][c] = mn;
+        l[n][c] *= al;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          O[i][n][c] *= al;
+          O[i][n][c + 2] *= al;
+        }
+      }
+  };
+
+  if (n_my > 0) {
+    const float gk = p.k.gscale[p.k.gstride * sq.s] * p.scale_log2;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      fac[n][0] *= gk;
+      fac[n][1] *= gk;
+    }
+  }
+  for (int i = 0; i < n_my; ++i) {
+    cp_async_wait<ST - 2>();
+    __syncwarp();
+    {
+      const int a = next[0], c = next[1], k = i + ST - 1;
+      look_up(k + 1);
+      if (k < n_my) issue(k, a, c);
+      cp_async_commit();
+    }
+    const unsigned char* st = ring + (i % ST) * Sh::kStageBytes;
+    const uint32_t vm = vms[w * ST + i % ST];
+    const int tok0 = (t_first + i * kKaWarps) * kKaTile;
+    const int64_t pos0 = (int64_t)sq.ns + tok0;
+    const bool full = vm == 0xFFFFFFFFu && pos0 + kKaTile <= lim_min;
+
+    // ---- S^T = K Q^T: rows are tokens (two tiles of 16), columns query rows ----
+    float S[2][NT][4];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[a][n][c] = 0.0f;
+#pragma unroll
+    for (int cc = 0; cc < KCH; ++cc) {
+      uint32_t kw[4][KW], ks[4][KW / 2];         // rows perm + 8 k of the tile; scales doubled into both halves
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = perm + 8 * k;
+        const uint32_t sw = ((uint32_t)row >> 2 & 1u) << 6;
+        if constexpr (KW == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kKC + ((row * Sh::kCodeRow + (t + 4 * cc) * 16) ^ sw));
+          kw[k][0] = v.x, kw[k][1] = v.y, kw[k][2] = v.z, kw[k][3] = v.w;
+          const uint32_t h = e4m3x2_f16x2(*reinterpret_cast<const unsigned short*>(st + Sh::kKS + row * Sh::kScaleRow + 2 * t + 8 * cc));
+          ks[k][0] = __byte_perm(h, h, 0x1010);
+          ks[k][1] = __byte_perm(h, h, 0x3232);
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kKC + ((row * Sh::kCodeRow + t * 8) ^ sw));
+          kw[k][0] = v.x, kw[k][1] = v.y;
+          const uint32_t h = e4m3x2_f16x2(st[Sh::kKS + row * Sh::kScaleRow + t]);
+          ks[k][0] = __byte_perm(h, h, 0x1010);
+        }
+      }
+#pragma unroll
+      for (int wd = 0; wd < KW; ++wd) {          // a word of 8 codes feeds two steps
+        uint32_t h[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          e2m1x8(kw[k][wd], h[k]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) h[k][c] = hmul2(h[k][c], ks[k][wd >> 1]);
+        }
+#pragma unroll
+        for (int j2 = 0; j2 < 2; ++j2) {
+          const int j = cc * 8 + wd * 2 + j2;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 qv = qf[(n * NS + j) * 32 + lane];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
+              mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.z, qv.w);
+            }
+          }
+        }
+      }
+    }
+    // ---- numerators ----
+    float mx[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mx[n][c] = -INFINITY;
+        const int rel = (int)max(min((int64_t)lim[n][c] - pos0, (int64_t)kKaTile), (int64_t)0);
+        const uint32_t seen = full ? 0xFFFFFFFFu : vm & (rel >= 32 ? 0xFFFFFFFFu : (1u << rel) - 1u);
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float& s = S[a][n][c + 2 * h];
+            s *= fac[n][c];
+            if (!full) s = (seen >> (16 * a + 8 * h + perm)) & 1u ? s : -INFINITY;
+            mx[n][c] = fmaxf(mx[n][c], s);
+          }
+      }
+    raise(mx);
+    uint32_t pb[2][NT][2];                       // the second product's B fragments (tokens x query rows)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float s0 = finite_or_zero(m[n][0]) - kKaPShift, s1 = finite_or_zero(m[n][1]) - kKaPShift;
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = ex2(S[a][n][2 * h] - s0), p1 = ex2(S[a][n][2 * h + 1] - s1);
+          l[n][0] += p0;
+          l[n][1] += p1;
+          pb[a][n][h] = movmatrix(pack_f16(p0, p1));
+        }
+    }
+    // ---- O^T += V^T P^T: rows are channels, the 16 k positions the tokens 4 r + t of the fragment order ----
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      uint32_t vw[4][VW], vs[2][VB];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * a + 4 * r + t;
+        if constexpr (VW == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kVC + ((row * Sh::kCodeRow + g * 16) ^ ((row & 3) << 5)));
+          vw[r][0] = v.x, vw[r][1] = v.y, vw[r][2] = v.z, vw[r][3] = v.w;
+        } else if constexpr (VW == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kVC + ((row * Sh::kCodeRow + g * 8) ^ ((row >> 1 & 1) << 5)));
+          vw[r][0] = v.x, vw[r][1] = v.y;
+        } else {
+          vw[r][0] = *reinterpret_cast<const uint32_t*>(st + Sh::kVC + row * Sh::kCodeRow + g * 4);
+        }
+      }
+#pragma unroll
+      for (int q2 = 0; q2 < 2; ++q2) {
+        const unsigned char* s0 = st + Sh::kVS + (16 * a + 8 * q2 + t) * Sh::kScaleRow;
+        const unsigned char* s1 = s0 + 4 * Sh::kScaleRow;
+        if constexpr (VB == 2) {
+          const uint32_t u0 = *reinterpret_cast<const unsigned short*>(s0 + 2 * g), u1 = *reinterpret_cast<const unsigned short*>(s1 + 2 * g);
+          vs[q2][0] = e4m3x2_f16x2(__byte_perm(u0, u1, 0x0040));
+          vs[q2][1] = e4m3x2_f16x2(__byte_perm(u0, u1, 0x0051));
+        } else {
+          const int blk = D == 128 ? g : g >> 1;
+          vs[q2][0] = e4m3x2_f16x2(s0[blk] | (uint32_t)s1[blk] << 8);
+        }
+      }
+      uint32_t nan_tok[VB];
+      if (!full) {
+        // a poisoned block (scale NaN) of a token that only some of the columns see: 0 * NaN would reach the
+        // others through the product, so its scale becomes 0 and the columns that do see it turn NaN below
+#pragma unroll
+        for (int vb = 0; vb < VB; ++vb) {
+          nan_tok[vb] = 0;
+#pragma unroll
+          for (int q2 = 0; q2 < 2; ++q2) {
+            const uint32_t u = vs[q2][vb];
+            if ((u & 0x7FFFu) > 0x7C00u) nan_tok[vb] |= 1u << (16 * a + 8 * q2 + t), vs[q2][vb] &= 0xFFFF0000u;
+            if ((u >> 16 & 0x7FFFu) > 0x7C00u) nan_tok[vb] |= 1u << (16 * a + 8 * q2 + 4 + t), vs[q2][vb] &= 0x0000FFFFu;
+          }
+          nan_tok[vb] |= __shfl_xor_sync(0xFFFFFFFFu, nan_tok[vb], 1);
+          nan_tok[vb] |= __shfl_xor_sync(0xFFFFFFFFu, nan_tok[vb], 2);
+        }
+      }
+#pragma unroll
+      for (int wd = 0; wd < VW; ++wd) {
+        constexpr uint32_t LO = 0x0F0F0F0Fu;
+        uint32_t hx[2][4], hy[2][4];             // even and odd channels, (token 4 r + t, token 4 (r + 1) + t)
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+          const uint32_t u = vw[2 * q2][wd], v = vw[2 * q2 + 1][wd];
+          e2m1x8((u & LO) | ((v << 4) & ~LO), hx[q2]);
+          e2m1x8(((u >> 4) & LO) | (v & ~LO), hy[q2]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            hx[q2][k] = hmul2(hx[q2][k], vs[q2][VB == 2 ? wd >> 1 : 0]);
+            hy[q2][k] = hmul2(hy[q2][k], vs[q2][VB == 2 ? wd >> 1 : 0]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma16816<false>(O[4 * wd + k][n], hx[0][k], hy[0][k], hx[1][k], hy[1][k], pb[a][n][0], pb[a][n][1]);
+      }
+      if (!full) {
+#pragma unroll
+        for (int vb = 0; vb < VB; ++vb)
+          if (nan_tok[vb]) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int rel = (int)max(min((int64_t)lim[n][c] - pos0, (int64_t)kKaTile), (int64_t)0);
+                const uint32_t seen = vm & (rel >= 32 ? 0xFFFFFFFFu : (1u << rel) - 1u);
+                if (nan_tok[vb] & seen) {
+#pragma unroll
+                  for (int k = 0; k < NO / VB; ++k) O[vb * (NO / VB) + k][n][c] = O[vb * (NO / VB) + k][n][c + 2] = NAN;
+                }
+              }
+          }
+      }
+    }
+  }
+
+  // ---- the middle's sums: undo the numerators' scale, apply g_v, turn back along the channels ----
+  if (n_my > 0) {
+    constexpr float kUndo = 1.0f / 32768.0f;
+    const float gv = p.v.gscale[p.v.gstride * sq.s] * kUndo;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[n][c] *= kUndo;
+        if (p.v.rotate) {
+          if constexpr (D == 64) {
+            // 8 channels here, the other 8 of the block in the lane of g ^ 1
+            float a[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[2 * i] = O[i][n][c], a[2 * i + 1] = O[i][n][c + 2];
+#pragma unroll
+            for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if ((i & h) == 0) {
+                  const float u = a[i], v = a[i + h];
+                  a[i] = u + v;
+                  a[i + h] = u - v;
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float o = __shfl_xor_sync(0xFFFFFFFFu, a[i], 4);
+              a[i] = 0.25f * (g & 1 ? o - a[i] : a[i] + o);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) O[i][n][c] = a[2 * i], O[i][n][c + 2] = a[2 * i + 1];
+          } else {
+#pragma unroll
+            for (int blk = 0; blk < NO / 8; ++blk) {
+              float a[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) a[2 * i] = O[8 * blk + i][n][c], a[2 * i + 1] = O[8 * blk + i][n][c + 2];
+              fwht16(a);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) O[8 * blk + i][n][c] = a[2 * i], O[8 * blk + i][n][c + 2] = a[2 * i + 1];
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          O[i][n][c] *= gv;
+          O[i][n][c + 2] *= gv;
+        }
+      }
+  }
+
+  // ---- the BF16 ends, 16 tokens at a time, spread over the ranges and their warps ----
+  const int sink_tiles = (sq.ns + 15) / 16, end_tiles = sink_tiles + (sq.nw + 15) / 16;
+  for (int64_t e64 = ch + (int64_t)active * w; e64 < end_tiles; e64 += (int64_t)active * kKaWarps) {
+    const int e = (int)e64;
+    const bool in_sink = e < sink_tiles;
+    const int r0 = 16 * (in_sink ? e : e - sink_tiles), cnt = min(16, (in_sink ? sq.ns : sq.nw) - r0);
+    const int64_t pos0 = in_sink ? r0 : (int64_t)sq.ns + sq.nm + r0;
+    const int rows = in_sink ? p.sink_rows : p.window_rows;
+    const int64_t mat = ((int64_t)sq.s * p.Hkv + kvh) * rows;
+    const bool cut = pos0 + cnt > lim_min;       // some row does not see all of the tile
+    auto row_at = [&](const KvSide& s, int r) -> const char* {
+      int at = r0 + r;
+      if (!in_sink) {
+        at += sq.head;
+        if (at >= rows) at -= rows;
+      }
+      return (in_sink ? s.sink : s.window) + (mat + at) * (D * 2);
+    };
+    float S[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) S[n][c] = 0.0f;
+    const bool ok0 = perm < cnt, ok1 = perm + 8 < cnt;
+    const char* k0 = row_at(p.k, ok0 ? perm : 0);
+    const char* k1 = row_at(p.k, ok1 ? perm + 8 : 0);
+#pragma unroll
+    for (int cc = 0; cc < KCH; ++cc)
+#pragma unroll
+      for (int v8 = 0; v8 < KW; ++v8) {          // 8 channels of the chunk: two steps
+        uint4 u = make_uint4(0, 0, 0, 0), v = u;
+        const int at = ((t + 4 * cc) * (KW * 8) + v8 * 8) * 2;
+        if (ok0) u = *reinterpret_cast<const uint4*>(k0 + at);
+        if (ok1) v = *reinterpret_cast<const uint4*>(k1 + at);
+        const int j = cc * 8 + v8 * 2;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 qa = qe[(n * NS + j) * 32 + lane], qb = qe[(n * NS + j + 1) * 32 + lane];
+          mma16816<true>(S[n], u.x, v.x, u.y, v.y, qa.x, qa.y);
+          mma16816<true>(S[n], u.z, v.z, u.w, v.w, qb.x, qb.y);
+          if constexpr (!QBF) {                  // a BF16 query is its first term
+            mma16816<true>(S[n], u.x, v.x, u.y, v.y, qa.z, qa.w);
+            mma16816<true>(S[n], u.z, v.z, u.w, v.w, qb.z, qb.w);
+          }
+        }
+      }
+    float mx[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mx[n][c] = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = perm + 8 * h;
+          float& s = S[n][c + 2 * h];
+          s = r < cnt && pos0 + r < lim[n][c] ? s * p.scale_log2 : -INFINITY;
+          mx[n][c] = fmaxf(mx[n][c], s);
+        }
+      }
+    raise(mx);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float ms = finite_or_zero(m[n][c]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          S[n][c + 2 * h] = ex2(S[n][c + 2 * h] - ms);
+          l[n][c] += S[n][c + 2 * h];
+        }
+      }
+    uint32_t ph[NT][2], pl[NT][2];               // numerators as two BF16 terms
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a, c;
+        split_bf16(S[n][2 * h], S[n][2 * h + 1], a, c);
+        ph[n][h] = movmatrix(a);
+        pl[n][h] = movmatrix(c);
+      }
+#pragma unroll
+    for (int v8 = 0; v8 < D / 64; ++v8) {        // 8 channels of the thread's chunk
+      uint4 vv[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool ok = 4 * r + t < cnt;
+        vv[r] = make_uint4(0, 0, 0, 0);
+        if (ok) vv[r] = *reinterpret_cast<const uint4*>(row_at(p.v, 4 * r + t) + (g * (D / 8) + v8 * 8) * 2);
+      }
+      if (!cut) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w0 = (&vv[0].x)[k], w1 = (&vv[1].x)[k], w2 = (&vv[2].x)[k], w3 = (&vv[3].x)[k];
+          const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+          const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+            mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+          }
+        }
+      } else {
+        // tokens that some rows do not see: added token by token, so that infinities and NaN of a hidden
+        // token reach no row (a product would multiply them by its zero numerator)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          for (int tt = 0; tt < 4; ++tt) {
+            uint32_t wd[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) wd[k] = __shfl_sync(0xFFFFFFFFu, (&vv[r].x)[k], g * 4 + tt);
+            const int tk = 4 * r + tt, fr = 2 * tt + (r & 1);     // the token's fragment row is fr + 8 (r >> 1)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float pr = __shfl_sync(0xFFFFFFFFu, S[n][c + 2 * (r >> 1)], fr * 4 + t);
+                if (tk < cnt && pos0 + tk < lim[n][c]) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    O[4 * v8 + k][n][c] = fmaf(pr, bf16lo(wd[k]), O[4 * v8 + k][n][c]);
+                    O[4 * v8 + k][n][c + 2] = fmaf(pr, bf16hi(wd[k]), O[4 * v8 + k][n][c + 2]);
+                  }
+                }
+              }
+          }
+        }
+      }
+    }
+  }
+
+  // ---- join the warps ----
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], o);
+      if (g == 0) stat[w * ROWS + 8 * n + 2 * t + c] = make_float2(m[n][c], l[n][c]);
+    }
+  cp_async_wait<0>();
+  __syncthreads();                               // every warp is done with its ring: the accumulators take its place
+  float* acc = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 8 * n + 2 * t + c;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kKaWarps; ++k) mm = fmaxf(mm, stat[k * ROWS + row].x);
+      const float f = ex2(m[n][c] - finite_or_zero(mm));
+      float* a = acc + (w * ROWS + row) * Sm::kAccRow + g * (D / 8);
+#pragma unroll
+      for (int i = 0; i < NO; ++i) *reinterpret_cast<float2*>(a + 2 * i) = make_float2(O[i][n][c] * f, O[i][n][c + 2] * f);
+    }
+  __syncthreads();
+  for (int u = tid; u < ROWS * (D / 4); u += kKaWarps * 32) {
+    const int row = u / (D / 4), d = 4 * (u % (D / 4)), r = row_tile * ROWS + row;
+    if (r >= p.R) continue;
+    float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kKaWarps; ++k) mm = fmaxf(mm, stat[k * ROWS + row].x);
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kKaWarps; ++k) {
+      const float2 ml = stat[k * ROWS + row];
+      ll = fmaf(ml.y, ex2(ml.x - finite_or_zero(mm)), ll);
+      const float4 v = *reinterpret_cast<const float4*>(acc + (k * ROWS + row) * Sm::kAccRow + d);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const int i = r / p.G, hq = kvh * p.G + r % p.G;
+    if (active > 1) {
+      const int64_t at = ((int64_t)(b * p.Hkv + kvh) * p.R + r) * p.nch + ch;
+      *reinterpret_cast<float4*>(p.ws_o + at * D + d) = s;
+      if (d == 0) p.ws_ml[at] = make_float2(mm, ll);
+    } else {
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;   // no visible token: zeros
+      const int64_t at = b * p.o_sb + hq * p.o_sh + i * p.o_st + d;
+      ka_store<QBF>(p.out, at, s.x * inv);
+      ka_store<QBF>(p.out, at + 1, s.y * inv);
+      ka_store<QBF>(p.out, at + 2, s.z * inv);
+      ka_store<QBF>(p.out, at + 3, s.w * inv);
+      if (d == 0 && p.lse) p.lse[((int64_t)b * p.Hq + hq) * p.Tq + i] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+    }
+  }
+}
+
+// Joins the ranges of the sequences that have more than one: a CTA per query row, warps striding the ranges.
+template <int D, bool QBF>
+__global__ void __launch_bounds__(128) kv_attn_combine_kernel(const __grid_constant__ KvAttnParams p) {
+  constexpr int E = D / 32;                      // channels per lane
+  __shared__ float part[4][D];
+  __shared__ float lpart[4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int row = blockIdx.x, r = row % p.R, bk = row / p.R, kvh = bk % p.Hkv, b = bk / p.Hkv;
+  const KaSeq sq = ka_sequence(p, b);
+  int per, active;
+  ka_ranges(sq.nm, p.nch, per, active);
+  if (active == 1) return;
+  const float2* ml = p.ws_ml + (int64_t)row * p.nch;
+  const float* o = p.ws_o + (int64_t)row * p.nch * D + lane * E;
+  float mm = -INFINITY;
+  for (int c = lane; c < active; c += 32) mm = fmaxf(mm, ml[c].x);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, k));
+  const float ms = finite_or_zero(mm);
+  float s[E], ll = 0.0f;
+#pragma unroll
+  for (int k = 0; k < E; ++k) s[k] = 0.0f;
+#pragma unroll 4
+  for (int c = w; c < active; c += 4) {
+    const float2 st = ml[c];
+    const float f = ex2(st.x - ms);
+    ll = fmaf(st.y, f, ll);
+    float v[E];
+#pragma unroll
+    for (int k = 0; k < E; k += 2) *reinterpret_cast<float2*>(v + k) = *reinterpret_cast<const float2*>(o + (int64_t)c * D + k);
+#pragma unroll
+    for (int k = 0; k < E; ++k) s[k] = fmaf(v[k], f, s[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < E; ++k) part[w][lane * E + k] = s[k];
+  if (lane == 0) lpart[w] = ll;
+  __syncthreads();
+  ll = (lpart[0] + lpart[1]) + (lpart[2] + lpart[3]);
+  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+  const int i = r / p.G, hq = kvh * p.G + r % p.G;
+  const int64_t at = b * p.o_sb + hq * p.o_sh + i * p.o_st;
+  for (int d = threadIdx.x; d < D; d += 128)
+    ka_store<QBF>(p.out, at + d, ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) * inv);
+  if (threadIdx.x == 0 && p.lse)
+    p.lse[((int64_t)b * p.Hq + hq) * p.Tq + i] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+}
+
+}  // namespace nvfp4

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/nvfp4.h"
+#include "api_util.cuh"
 #include "attention.cuh"
 #include "attn_fused.cuh"
 #include "lanes.cuh"
@@ -20,27 +21,6 @@
 using namespace nvfp4;
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-struct DeviceInfo {
-  int sms = 0;
-};
-
-DeviceInfo g_dev[kMaxDevices];
-std::mutex g_dev_mu;
-
-int sm_count() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
-  std::lock_guard<std::mutex> lk(g_dev_mu);
-  if (g_dev[dev].sms == 0) {
-    int s = 0;
-    cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev);
-    g_dev[dev].sms = s > 0 ? s : 148;
-  }
-  return g_dev[dev].sms;
-}
 
 // Persistent-style grid: enough CTAs for `items` at `per_cta` items each, capped at `ctas_per_sm` per SM.
 int grid_for(int64_t items, int per_cta, int ctas_per_sm) {
@@ -75,23 +55,6 @@ bool inject_launch_fault() {
 // Largest element count of a one-dimensional call: byte offsets of any element type stay far from
 // int64 overflow.
 constexpr int64_t kMaxElems = int64_t(1) << 60;
-
-// Product of sizes that must each be non-negative, or -1 when one is negative or the product does not
-// fit in int64 (so that no later size arithmetic can wrap round and pass a check).
-int64_t checked_prod(std::initializer_list<int64_t> v) {
-  int64_t p = 1;
-  for (int64_t a : v) {
-    if (a < 0 || __builtin_mul_overflow(p, a, &p)) return -1;
-  }
-  return p;
-}
-
-inline cudaStream_t S(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline bool dtype_ok(int dt) { return dt == DT_F32 || dt == DT_BF16 || dt == DT_F16; }
-inline int esize(int dt) { return dt == DT_F32 ? 4 : 2; }
-
-int last_error() { return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 
 int check_finite_sync(const float* g_dev, cudaStream_t s) {
   if (!checked_mode() || g_dev == nullptr) return NVFP4_OK;
