@@ -11,14 +11,23 @@ head_dim when `rotate`) into the NVFP4 middle.  The window therefore always keep
 The tensor scale is fixed by the prefill (`nvfp4_kv_gscale` over the rotated middle tokens, as in
 `nvfp4_kv_mixed`); later tokens use it unchanged, so values beyond 448 * 6 * g saturate.
 
-Host-side bookkeeping only: token rows are moved with tensor copies, every quantization runs in the
-library's kernels.
+`attend` reads a K and a V cache where they lie (nvfp4_kv_attention).  NVFP4PagedKVCache holds the K and V
+caches of every layer for many sequences of different lengths over one pool of pages, which sequences that
+were forked share.
+
+Host-side bookkeeping only: token rows are moved with tensor copies, every quantization, attention and page
+copy runs in the library's kernels.
 """
 from __future__ import annotations
 
+import ctypes
+import heapq
+
+import numpy as np
 import torch
 
-from . import KV_APPEND_BATCH_MAX, KvAppendBatch, kv_append, kv_gscale, sf_mma_bytes
+from . import (KV_APPEND_BATCH_MAX, KvAppendBatch, KvStore, _KvAppendDesc, _launch, copy_pages, kv_append, kv_attention,
+               kv_gscale, lib, sf_mma_bytes)
 
 
 class NVFP4KVCache:
@@ -53,6 +62,13 @@ class NVFP4KVCache:
         self.head = 0        # first valid window slot: 0 or recent
         self.n_window = 0
         self.prefilled = False
+        self._store = None
+
+    def store(self) -> KvStore:
+        """The cache as kv_attention reads it."""
+        if self._store is None:
+            self._store = KvStore(self.sink, self.window, self.codes, self.scales, self.gscale, self.rotate, self.tile_layout)
+        return self._store
 
     @property
     def length(self) -> int:
@@ -173,3 +189,323 @@ def append_many(caches, ks) -> None:
     """Append one decode step's new tokens to several caches at once (a one-off NVFP4KVCacheGroup; keep a
     group for a decode loop, so that its descriptors are prepared once)."""
     NVFP4KVCacheGroup(caches).append(ks)
+
+
+def attend(q: torch.Tensor, k_cache: NVFP4KVCache, v_cache: NVFP4KVCache, causal: bool = True,
+           scale: float | None = None, want_lse: bool = False, out: torch.Tensor | None = None):
+    """Attention of the newest Tq tokens (already appended to both caches) over everything the caches hold: q
+    [B, Hq, Tq, D] (BF16 or FP16, Hq a multiple of the caches' heads), kv_attention's output(s)."""
+    a, b = ((c.n_sink, c.n_mid, c.head, c.n_window) for c in (k_cache, v_cache))
+    if a != b:
+        raise ValueError("the K and V caches hold different tokens")
+    if not k_cache.prefilled or not v_cache.prefilled:
+        raise RuntimeError("prefill first")
+    if q.shape[0] != k_cache.B:
+        raise ValueError("q must have the caches' batch")
+    return kv_attention(q, k_cache.store(), v_cache.store(), a, causal=causal, scale=scale, want_lse=want_lse, out=out)
+
+
+# nvfp4_kv_append_desc as a numpy record, so that a flush over many layers and sequences is filled column by column
+_APPEND = np.dtype([("k_bf16", np.uint64), ("gscale", np.uint64), ("codes", np.uint64), ("scales", np.uint64),
+                    *((n, np.int64) for n in ("BH", "T", "first", "n", "D", "cap", "t0")),
+                    ("rotate", np.int32), ("scale_layout", np.int32)])
+assert _APPEND.itemsize == ctypes.sizeof(_KvAppendDesc)
+
+
+def _append_records(recs: np.ndarray, f_lo: int, f_hi: int, device: torch.device) -> None:
+    """nvfp4_kv_append_batch over `recs` (dtype _APPEND), 64 to a launch."""
+    fn = lib().nvfp4_kv_append_batch
+    for j in range(0, len(recs), KV_APPEND_BATCH_MAX):
+        part = recs[j:j + KV_APPEND_BATCH_MAX]
+        _launch(device, fn, part.ctypes.data, len(part), f_lo, f_hi)
+
+
+class DecodeStep:
+    """n new tokens of some sequences of an NVFP4PagedKVCache, as `step` reserved them: `slots` (host), `slot_ids`
+    (device int32 [B]) and where their rows go in the windows."""
+
+    def __init__(self, slots, n, slot_ids, rows, at, max_mid):
+        self.slots, self.n, self.slot_ids, self._rows, self._at, self.max_mid = slots, n, slot_ids, rows, at, max_mid
+
+
+class NVFP4PagedKVCache:
+    """K and V caches of `layers` layers for up to `slots` sequences, the NVFP4 middle in pages of `page_tokens`
+    tokens from one pool (page p holds the same tokens of every layer, K and V).  A decode step:
+
+        step = cache.step(slots)                     # once: room for the new tokens, windows flushed, lengths advanced
+        for layer in range(layers):
+            cache.store(step, layer, k, v)           # [B, H, n, D] BF16, rotary positions already applied
+            o = cache.attend(step, layer, q)         # [B, Hq, n, D]
+
+    Every sequence has its own tensor scales, fixed by its prefill and inherited by its forks.  Full pages of a
+    forked sequence are shared (counted), its half-filled last page is copied, so a page with two owners is
+    never written.  All calls of one cache belong on one stream.
+
+    Attributes (device tensors):
+      codes  [layers, 2, pages, H, page_tokens, D/2]   scales [..., D/16]   (2: K, V)
+      sink   [layers, 2, slots, H, sink, D] bf16       window [layers, 2, slots, H, 2*recent, D] bf16 ring
+      gscale [layers, 2, slots] float32                table  [slots, cols] int32 (-1: none)
+      lens   [slots, 4] int32: n_sink, n_mid, head, n_window
+    """
+
+    def __init__(self, layers: int, slots: int, H: int, D: int, pages: int, page_tokens: int = 64,
+                 max_tokens: int | None = None, sink: int = 16, recent: int = 16, rotate: bool = True, f_lo: int = -2,
+                 f_hi: int = 6, device="cuda"):
+        if D % 16 or recent <= 0 or sink < 0 or min(layers, slots, H, pages) <= 0:
+            raise ValueError("D must be a multiple of 16; recent, layers, slots, H, pages > 0; sink >= 0")
+        if page_tokens <= 0 or page_tokens % 16:
+            raise ValueError("page_tokens must be a multiple of 16")
+        if f_hi - f_lo + 1 > 32:
+            raise ValueError("the offset window holds at most 32 offsets")
+        self.layers, self.n_slots, self.H, self.D, self.n_pages, self.page_tokens = layers, slots, H, D, pages, page_tokens
+        self.n_sink_max, self.recent, self.rotate, self.f_lo, self.f_hi = sink, recent, rotate, f_lo, f_hi
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        cols = pages if max_tokens is None else min(pages, max(-(-max_tokens // page_tokens), 1))
+        z = lambda *s, dt=torch.uint8: torch.zeros(s, dtype=dt, device=dev)  # noqa: E731
+        self.codes, self.scales = (z(layers, 2, pages, H, page_tokens, D // w) for w in (2, 16))
+        self.sink = z(layers, 2, slots, H, sink, D, dt=torch.bfloat16)
+        self.window = z(layers, 2, slots, H, 2 * recent, D, dt=torch.bfloat16)
+        self.gscale = z(layers, 2, slots, dt=torch.float32)
+        self.lens = z(slots, 4, dt=torch.int32)
+        self.table = torch.full((slots, cols), -1, dtype=torch.int32, device=dev)
+        self._lens = np.zeros((slots, 4), np.int32)       # the host's copies; the device's follow in _publish
+        self._table = np.full((slots, cols), -1, np.int32)
+        self._held: list[list[int] | None] = [None] * slots   # pages of each sequence, None: the slot is free
+        self._refs = [0] * pages
+        self._free = list(range(pages))                    # a heap: the lowest page first
+        self._stores: dict[int, tuple[KvStore, KvStore]] = {}
+
+    # ---- sequences ----
+    @property
+    def pages_free(self) -> int:
+        return len(self._free)
+
+    def length(self, slot: int) -> int:
+        self._owned(slot)
+        return int(self._lens[slot, 0] + self._lens[slot, 1] + self._lens[slot, 3])
+
+    def alloc(self) -> int:
+        """A free slot, now an empty sequence."""
+        for s, held in enumerate(self._held):
+            if held is None:
+                self._held[s] = []
+                return s
+        raise RuntimeError("no free slot")
+
+    def free(self, slot: int) -> None:
+        """End a sequence: its slot and the pages that no other sequence shares are free again."""
+        for p in self._owned(slot):
+            self._drop(p)
+        self._held[slot] = None
+        self._lens[slot] = 0
+        self._table[slot] = -1
+        self._publish([slot])
+
+    def prefill(self, slot: int, ks, vs) -> None:
+        """Start sequence `slot` (from alloc) from its prompt: ks[l], vs[l] [H, T, D] or [1, H, T, D] BF16, T >= sink +
+        recent, rotary positions applied.  Tensor scales over the middle as NVFP4KVCache.prefill, per layer and side."""
+        if self._owned(slot) or self._lens[slot].any():
+            raise RuntimeError("the sequence has been started")
+        sides = [[self._prompt(x) for x in xs] for xs in (ks, vs)]
+        T = sides[0][0].shape[2] if sides[0] else 0
+        if any(len(xs) != self.layers or any(x.shape[2] != T for x in xs) for xs in sides):
+            raise ValueError("one K and one V tensor per layer, all of one length")
+        s, r = self.n_sink_max, self.recent
+        if T < s + r:
+            raise ValueError("prefill needs at least sink + recent tokens")
+        mid = T - s - r
+        self._grow([(slot, mid)])
+        for side, xs in enumerate(sides):
+            for layer, x in enumerate(xs):
+                # a prompt without a middle sets the scale by all of its tokens (0 would quantize every later one to 0)
+                kv_gscale(x, s if mid else 0, r if mid else 0, self.rotate, out=self.gscale[layer, side, slot:slot + 1])
+                self.sink[layer, side, slot].copy_(x[0, :, :s])
+                self.window[layer, side, slot, :, :r].copy_(x[0, :, T - r:])
+        P = self.page_tokens
+        rows = [(slot, s + i * P, min(P, mid - i * P), p, 0) for i, p in enumerate(self._held[slot])]
+        for side, xs in enumerate(sides):
+            for layer, x in enumerate(xs):
+                if rows:
+                    self._quantize(rows, layer, side, x.data_ptr(), 0, T)
+        self._lens[slot] = (s, mid, 0, r)
+        self._publish([slot])
+
+    def fork(self, slot: int, n: int = 1) -> list[int]:
+        """n new sequences that continue `slot`: its full pages are shared, the last page (when half filled) and the
+        BF16 ends are copied, in one launch each."""
+        held = self._owned(slot)
+        free = [s for s, h in enumerate(self._held) if h is None]
+        if n < 0 or len(free) < n:
+            raise RuntimeError("not enough free slots")
+        new = free[:n]
+        full = int(self._lens[slot, 1]) // self.page_tokens
+        tail = held[full:]                                   # at most one page
+        if len(tail) * n > len(self._free):
+            raise RuntimeError("NVFP4 page pool exhausted")
+        src, dst = [], []
+        for s in new:
+            self._held[s] = list(held[:full])
+            for p in held[:full]:
+                self._refs[p] += 1
+            for p in tail:
+                q = self._take()
+                self._held[s].append(q)
+                src.append(p)
+                dst.append(q)
+            self._lens[s] = self._lens[slot]
+            self._table[s] = -1
+            self._table[s, :len(self._held[s])] = self._held[s]
+        if src:
+            copy_pages([(self.codes, 2), (self.scales, 2)], src, dst)
+        if new:
+            ends = [(t, 2) for t in (self.sink, self.window, self.gscale) if t.numel()]
+            copy_pages(ends, [slot] * n, new)
+        self._publish(new)
+        return new
+
+    def compact(self) -> int:
+        """Moves the pages in use to the front of the pool, in one launch; returns their number (the pages from there
+        on hold nothing)."""
+        used = [p for p, r in enumerate(self._refs) if r]
+        n = len(used)
+        holes = [p for p in range(n) if not self._refs[p]]
+        move = dict(zip((p for p in used if p >= n), holes))
+        if move:
+            copy_pages([(self.codes, 2), (self.scales, 2)], list(move), list(move.values()))
+            for a, b in move.items():
+                self._refs[b], self._refs[a] = self._refs[a], 0
+            self._free = list(range(n, self.n_pages))
+            changed = []
+            for s, held in enumerate(self._held):
+                if held and any(p in move for p in held):
+                    held[:] = [move.get(p, p) for p in held]
+                    self._table[s, :len(held)] = held
+                    changed.append(s)
+            self._publish(changed)
+        return n
+
+    # ---- decoding ----
+    def step(self, slots, n: int = 1) -> DecodeStep:
+        """Reserve n (at most `recent`) new tokens for each of the distinct sequences `slots`: windows without room flush
+        their oldest `recent` tokens into pages (64 rows of one layer and side each per launch), and the lengths on the
+        device count the new tokens from here on."""
+        slots, r = [int(s) for s in slots], self.recent
+        if len(set(slots)) != len(slots):
+            raise ValueError("a sequence appears twice")
+        if not 0 < n <= r:
+            raise ValueError("a step holds 1 to `recent` tokens")
+        for s in slots:
+            self._owned(s)
+            if not self._lens[s].any():
+                raise RuntimeError("prefill first")
+        full = [s for s in slots if self._lens[s, 3] + n > 2 * r]
+        self._grow([(s, int(self._lens[s, 1]) + r) for s in full])
+        rows, P = [], self.page_tokens
+        for s in full:
+            first, mid, left = int(self._lens[s, 2]), int(self._lens[s, 1]), r
+            while left:                                      # a group may cross pages
+                k = min(left, P - mid % P)
+                rows.append((s, first, k, self._held[s][mid // P], mid % P))
+                first, mid, left = first + k, mid + k, left - k
+            self._lens[s] = (self._lens[s, 0], mid, (self._lens[s, 2] + r) % (2 * r), self._lens[s, 3] - r)
+        if rows:
+            self._quantize(rows, None, None, self.window.data_ptr(), self.H * 2 * r * self.D * 2, 2 * r)
+        head = (self._lens[slots, 2] + self._lens[slots, 3]).astype(np.int64)
+        self._lens[slots, 3] += n
+        self._publish(slots)
+        at = self._upload((head[:, None] + np.arange(n)) % (2 * r))
+        ids = self._upload(np.array(slots, np.int32))
+        return DecodeStep(slots, n, ids, ids.long()[:, None], at, int(self._lens[slots, 1].max()) if slots else 0)
+
+    def store(self, step: DecodeStep, layer: int, k: torch.Tensor, v: torch.Tensor) -> None:
+        """The step's K and V rows [B, H, n, D] (BF16) of one layer."""
+        shape = (len(step.slots), self.H, step.n, self.D)
+        for side, x in enumerate((k, v)):
+            if x.shape != shape or x.dtype != torch.bfloat16:
+                raise ValueError(f"k and v must be bfloat16 {list(shape)}")
+            self.window[layer, side][step._rows, :, step._at] = x.transpose(1, 2)
+
+    def attend(self, step: DecodeStep, layer: int, q: torch.Tensor, scale: float | None = None, causal: bool = True,
+               want_lse: bool = False, out: torch.Tensor | None = None):
+        """Attention of the step's tokens, q [B, Hq, n, D], over their sequences (kv_attention's output(s))."""
+        k, v = self.stores(layer)
+        if q.shape[0] != len(step.slots) or q.shape[2] != step.n:
+            raise ValueError("q must be [B, Hq, n, D] of the step")
+        return kv_attention(q, k, v, self.lens, self.table, step.slot_ids, causal, scale, step.max_mid, want_lse, out)
+
+    def stores(self, layer: int) -> tuple[KvStore, KvStore]:
+        """The layer's K and V as kv_attention reads them (with `lens` and `table`)."""
+        if layer not in self._stores:
+            if not 0 <= layer < self.layers:
+                raise IndexError("no such layer")
+            self._stores[layer] = tuple(KvStore(self.sink[layer, i], self.window[layer, i], self.codes[layer, i],
+                                                self.scales[layer, i], self.gscale[layer, i], self.rotate) for i in (0, 1))
+        return self._stores[layer]
+
+    # ---- bookkeeping ----
+    def _owned(self, slot: int) -> list[int]:
+        if not 0 <= slot < self.n_slots or self._held[slot] is None:
+            raise ValueError(f"slot {slot} holds no sequence")
+        return self._held[slot]
+
+    def _prompt(self, x: torch.Tensor) -> torch.Tensor:
+        x = x if x.dim() == 4 else x[None]
+        if x.shape[:2] != (1, self.H) or x.shape[3] != self.D or x.dtype != torch.bfloat16:
+            raise ValueError("prompts must be bfloat16 [H, T, D] matching the cache")
+        return x.contiguous()
+
+    def _take(self) -> int:
+        p = heapq.heappop(self._free)
+        self._refs[p] = 1
+        return p
+
+    def _drop(self, p: int) -> None:
+        self._refs[p] -= 1
+        if not self._refs[p]:
+            heapq.heappush(self._free, p)
+
+    def _grow(self, wants) -> None:
+        """Pages for middles of the given tokens, all or none."""
+        need = [(s, -(-mid // self.page_tokens)) for s, mid in wants]
+        if any(n > self._table.shape[1] for _, n in need):
+            raise RuntimeError("NVFP4 cache capacity exceeded")
+        if sum(max(n - len(self._held[s]), 0) for s, n in need) > len(self._free):
+            raise RuntimeError("NVFP4 page pool exhausted")
+        for s, n in need:
+            held = self._held[s]
+            while len(held) < n:
+                held.append(self._take())
+                self._table[s, len(held) - 1] = held[-1]
+
+    def _quantize(self, rows, layer, side, base: int, slot_bytes: int, T: int) -> None:
+        """Rows (slot, first, n, page, t0): tokens [first, first + n) of the BF16 [H, T, D] buffer at base + slot *
+        slot_bytes go to rows t0 .. of `page`, for one (layer, side), or for all of them (windows, laid out
+        [layers, 2, slots, ...]) when layer is None."""
+        slot, first, n, page, t0 = np.array(rows, np.int64).T
+        pairs = np.arange(self.layers * 2) if layer is None else np.array([2 * layer + side])
+        recs = np.zeros((len(pairs), len(rows)), _APPEND)
+        lay = pairs[:, None]
+        recs["k_bf16"] = base + (lay * self.n_slots + slot) * slot_bytes if layer is None else base
+        recs["gscale"] = self.gscale.data_ptr() + 4 * (lay * self.n_slots + slot)
+        at = (lay * self.n_pages + page) * self.H * self.page_tokens * self.D
+        recs["codes"] = self.codes.data_ptr() + at // 2
+        recs["scales"] = self.scales.data_ptr() + at // 16
+        recs["BH"], recs["T"], recs["D"], recs["cap"], recs["rotate"] = self.H, T, self.D, self.page_tokens, int(self.rotate)
+        recs["first"], recs["n"], recs["t0"] = first, n, t0
+        _append_records(recs.reshape(-1), self.f_lo, self.f_hi, self.device)
+
+    def _upload(self, a: np.ndarray) -> torch.Tensor:
+        """A host array on the device without waiting for it: a fresh pinned buffer, kept until the copy is done."""
+        t = torch.from_numpy(np.array(a))
+        return t.pin_memory().to(self.device, non_blocking=True) if self.device.type == "cuda" else t.to(self.device)
+
+    def _publish(self, slots) -> None:
+        """The host's lengths and table rows of these sequences to the device."""
+        if not slots:
+            return
+        at = self._upload(np.array(slots, np.int64))
+        self.lens.index_copy_(0, at, self._upload(self._lens[slots]))
+        self.table.index_copy_(0, at, self._upload(self._table[slots]))
