@@ -431,7 +431,7 @@ typedef struct nvfp4_kv_attention_desc {
 /* out = softmax(scale q K^T) V over the tokens of each sequence in the order sink | middle | window (slots head,
  * head + 1, ... of the ring).  A row that sees no token gets zeros and lse -Inf.  Middle tokens stand for
  * E2M1(code) * E4M3(scale) * g, un-rotated when `rotate`; sums and softmax statistics are FP32, the middle's
- * query is carried in 22 bits and its numerators in FP16 (scaled by 2^15), the BF16 ends' in 16 bits.
+ * query is carried in 22 bits and its numerators in FP16 (scaled by 2^10), the BF16 ends' in 16 bits.
  * Hidden tokens (past a row's position, past a sequence's end) reach no row, whatever they hold; a visible
  * NaN reaches the rows that see it.
  * splits: 1 .. 128 ranges of the middle per sequence, worked on by different CTAs and then joined by a second
@@ -439,7 +439,8 @@ typedef struct nvfp4_kv_attention_desc {
  * result, which depends on it in the last bits).  workspace: caller-owned device memory, 16-byte aligned, of
  * nvfp4_kv_attention_workspace_bytes (NULL with splits == 1); calls that share one must be ordered.
  * No device memory is allocated and no state kept; lengths, slots and table are read on the device, so a
- * captured call follows their contents.  NVFP4_ERR_SIZE for unsupported sizes, NVFP4_ERR_ARG for host lengths
+ * captured call follows their contents.  Tensor scales are not negative.  Each part of a sequence holds at most
+ * 2^29 - 1 tokens and pages * Hkv * page_rows is below 2^32.  NVFP4_ERR_SIZE for unsupported sizes, NVFP4_ERR_ARG for host lengths
  * outside the buffers. */
 int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* workspace, size_t workspace_bytes,
                        void* stream);

@@ -129,8 +129,10 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* wo
   if (d.B < 0 || d.Hq < 0 || d.Hkv < 0 || d.Tq < 0 || d.slots < 0 || d.sink_rows < 0 || d.window_rows < 0 || d.pages < 0 ||
       d.page_rows < 0 || d.table_cols < 0)
     return NVFP4_ERR_SIZE;
-  if (d.B > kMaxInt || d.Hq > kMaxInt || d.Tq > kMaxInt || d.slots > kMaxInt || d.sink_rows > kMaxInt / 4 ||
-      d.window_rows > kMaxInt / 4 || d.pages > kMaxInt || d.page_rows > kMaxInt)
+  // positions are counted in 32 bits, with room for the largest sum of the three parts
+  constexpr int64_t kMaxPart = kMaxInt / 4;
+  if (d.B > kMaxInt || d.Hq > kMaxInt || d.Tq > kMaxPart || d.slots > kMaxInt || d.sink_rows > kMaxPart ||
+      d.window_rows > kMaxPart || d.pages > kMaxInt || d.page_rows > kMaxPart)
     return NVFP4_ERR_SIZE;
   if (d.B == 0 || d.Hq == 0 || d.Tq == 0) return NVFP4_OK;
   if (d.Hkv == 0 || d.Hq % d.Hkv != 0) return NVFP4_ERR_SIZE;
@@ -139,12 +141,13 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* wo
   if (d.table != nullptr) {
     if (d.page_rows == 0 || d.page_rows % 16 != 0) return NVFP4_ERR_SIZE;
     mid_rows = checked_prod({d.table_cols, d.page_rows});
-    if (mid_rows < 0 || mid_rows > kMaxInt || checked_prod({d.slots, d.table_cols, 4}) < 0) return NVFP4_ERR_SIZE;
+    if (mid_rows < 0 || mid_rows > kMaxPart || checked_prod({d.slots, d.table_cols, 4}) < 0) return NVFP4_ERR_SIZE;
   } else if (d.pages < d.slots) {
     return NVFP4_ERR_SIZE;                             // slot s is page s
   }
   if (checked_prod({d.slots, d.Hkv, d.sink_rows + d.window_rows, d.D, 2}) < 0 ||
-      checked_prod({d.pages, d.Hkv, (d.page_rows + 127) / 128 * 128, d.D}) < 0)
+      checked_prod({d.pages, d.Hkv, (d.page_rows + 127) / 128 * 128, d.D}) < 0 ||
+      d.pages * d.Hkv * d.page_rows >= (int64_t(1) << 32))       // rows are numbered in 32 bits
     return NVFP4_ERR_SIZE;
   if (d.lens == nullptr &&
       (d.n_sink < 0 || d.n_sink > d.sink_rows || d.n_mid < 0 || d.n_mid > mid_rows || d.n_window < 0 ||

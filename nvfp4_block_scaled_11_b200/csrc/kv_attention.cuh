@@ -21,8 +21,8 @@
 //   128 rows of expanded tiles in shared memory for 8 useful columns: the expansion would cross shared
 //   memory once more and the accumulators TMEM, for a product that is not what bounds the pass;
 // * the rotated query is split into two FP16 terms (22 bits after a power-of-two row scale), so scores
-//   keep FP32 accuracy; the numerators are rounded to FP16 once, scaled by 2^15 (full precision down to
-//   2^-29 of the row's maximum, 2^-12 relative error each; sums are taken in FP32 before that rounding);
+//   keep FP32 accuracy; the numerators are rounded to FP16 once, scaled by 2^10 (2^-12 relative error
+//   each down to 2^-24 of the row's maximum; sums are taken in FP32 before that rounding);
 // * S^T = K Q^T leaves (token, query) fragments; movmatrix turns the FP16 numerators into the second
 //   product's operand; V is packed along channels, so pairs of tokens are interleaved nibble by nibble
 //   (two logic operations per 8 codes and token) before the converts.
@@ -40,7 +40,8 @@ constexpr int kKaWarps = 4;            // warps per CTA, each with its own tiles
 constexpr int kKaTile = 32;            // middle tokens per tile
 constexpr int kKaMinTiles = 8;         // least tiles per range: shorter ones cost more in joining than they win
 constexpr int kKaMaxSplits = 128;
-constexpr float kKaPShift = 15.0f;     // numerators of the middle are scaled by 2^15 before FP16
+constexpr float kKaPShift = 10.0f;     // numerators of the middle are scaled by 2^10 before FP16
+constexpr float kKaSlack = 5.0f;       // how far (base 2) a score may pass its row's reference: 2^15 fits FP16
 
 struct KvSide {
   const char* sink;        // BF16 [slots, Hkv, sink_rows, D]
@@ -77,7 +78,7 @@ struct KaShape {
   static constexpr int kCodeRow = D / 2, kScaleRow = D / 16;
   static constexpr int kKC = 0, kVC = kKaTile * kCodeRow, kKS = 2 * kKaTile * kCodeRow, kVS = kKS + kKaTile * kScaleRow;
   static constexpr int kStageBytes = 2 * kKaTile * (kCodeRow + kScaleRow);
-  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kRing = kKaWarps * kStages * kStageBytes;
 };
 template <int D, int NT>
@@ -100,6 +101,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)_
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // the rest is zero-filled
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -111,17 +115,23 @@ template <bool BF>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   if constexpr (BF)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same from zero
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 // the four bytes of w (two E2M1 codes each) as f16x2
@@ -140,6 +150,16 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b2) {
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t both_lo(uint32_t h) {
+  uint32_t r;
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; mov.b32 %0, {a, a}; }" : "=r"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t both_hi(uint32_t h) {
+  uint32_t r;
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; mov.b32 %0, {b, b}; }" : "=r"(r) : "r"(h));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -173,7 +193,7 @@ __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY
 // The lengths of the sequence of batch row b, bounded by the buffers (an unknown slot is an empty sequence).
 struct KaSeq {
   int s, ns, nm, head, nw;
-  int64_t len;
+  int len;
 };
 __device__ __forceinline__ KaSeq ka_sequence(const KvAttnParams& p, int b) {
   KaSeq q;
@@ -193,7 +213,7 @@ __device__ __forceinline__ KaSeq ka_sequence(const KvAttnParams& p, int b) {
   q.nm = ok ? (int)min((int64_t)max(n[1], 0), most) : 0;
   q.nw = ok ? min(max(n[3], 0), p.window_rows) : 0;
   q.head = p.window_rows > 0 ? (int)((uint32_t)n[2] % (uint32_t)p.window_rows) : 0;
-  q.len = (int64_t)q.ns + q.nm + q.nw;
+  q.len = q.ns + q.nm + q.nw;
   return q;
 }
 // Tiles per range and the ranges that hold any (at least one) of a middle of nm tokens.
@@ -211,7 +231,7 @@ __device__ __forceinline__ void ka_store(char* out, int64_t i, float x) {
 
 // D: head_dim; NT: query rows / 8 of a CTA; QBF: q and out are BF16 (else FP16).
 template <int D, int NT, bool QBF>
-__global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? (NT == 1 ? 3 : 2) : D == 128 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 5 : 4)) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
   using Sh = KaShape<D>;
   using Sm = KaSmem<D, NT>;
   constexpr int ST = Sh::kStages, NS = D / 16 /* k16 steps */, NO = D / 16 /* m16 tiles of channels */;
@@ -246,69 +266,85 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
   // ---- the warp's ring: tile i of this warp goes to stage i % ST ----
   unsigned char* ring = smem + w * ST * Sh::kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
+  // Rows of the middle are numbered page by page (below 2^32, checked on the host): row (page Hkv + head) page_rows +
+  // r.  Keys are read as rows r and r + 4 together, values as rows r .. r + 3: each order gets its own exchange of
+  // 64- (32-) byte halves in shared memory so that both read without bank conflicts; a lane's exchange is the
+  // same in every instruction but for D = 256 keys.
+  constexpr int CPR = Sh::kCodeRow / 16, ITS = kKaTile * CPR / 32, HALF = ITS / 2;   // pieces per row, instructions
+  const uint32_t lane_row = lane / CPR;
+  const uint32_t k_at = ring_u + Sh::kKC + (lane * 16 ^ (D == 256 ? 0u : (lane_row >> 2 & 1u) << 6));
+  const uint32_t v_at = ring_u + Sh::kVC + (D == 128 ? lane * 16 ^ (lane_row >> 1 & 1u) << 5 : D == 256 ? lane * 16 ^ (lane_row & 3u) << 5 : lane * 16);
+  const uint8_t* kc = p.k.codes + lane * 16;
+  const uint8_t* vc = p.v.codes + lane * 16;
+  constexpr int RPP = 16 / Sh::kScaleRow, NP = kKaTile / RPP;        // scale rows per 16 bytes, pieces per tile and side
+  const uint8_t* sc = (NP == 32 || lane < NP ? p.k.scales : p.v.scales) + lane % (NP / 2) * 16;   // NP < 32: keys', then values'
+  const bool pieces16 = p.k.vec16 && p.v.vec16;
+  const uint32_t head_rows = (uint32_t)p.Hkv * (uint32_t)p.page_rows, my_rows = (uint32_t)kvh * (uint32_t)p.page_rows;
+  const int32_t* my_table = p.table ? p.table + (int64_t)sq.s * p.cols : nullptr;
+  const int mask = p.page_shift >= 0 ? p.page_rows - 1 : 0;
   auto page_of = [&](int tok) -> int {          // the page holding middle token tok, -1: none
     if (tok >= sq.nm) return -1;
-    if (!p.table) return sq.s;
-    const int c = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_rows;
-    const int pg = __ldg(p.table + (int64_t)sq.s * p.cols + c);
-    return pg >= 0 && pg < p.pages ? pg : -1;
+    if (!my_table) return sq.s;
+    const int pg = __ldg(my_table + (p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_rows));
+    return (uint32_t)pg < (uint32_t)p.pages ? pg : -1;
   };
-  auto row_in_page = [&](int tok) -> int {
-    if (!p.table) return tok;
-    return p.page_shift >= 0 ? tok & (p.page_rows - 1) : tok % p.page_rows;
-  };
-  auto issue = [&](int i, int pg0, int pg1) {
-    const int tok = (t_first + i * kKaWarps) * kKaTile, st = i % ST;
-    const uint32_t dst = ring_u + st * Sh::kStageBytes;
-    const int pg[2] = {pg0, pg1};
-    int64_t mat[2];
-    int r0[2];
-    uint32_t vm = 0;
+  auto row_in_page = [&](int tok) -> int { return !my_table ? tok : p.page_shift >= 0 ? tok & mask : tok % p.page_rows; };
+  uint32_t partial = 0;                         // bit i % 32: tile i does not hold 32 tokens (which it holds: vms)
+  auto issue = [&](int i, int st, int pg0, int pg1) {
+    const int tok = (t_first + i * kKaWarps) * kKaTile;
+    const uint32_t so = st * Sh::kStageBytes;
+    const int r0 = row_in_page(tok), r1 = row_in_page(tok + 16);
+    const uint32_t row0 = (uint32_t)pg0 * head_rows + my_rows + r0, row1 = (uint32_t)pg1 * head_rows + my_rows + r1;
+    const bool whole = (pg0 | pg1) >= 0 && tok + kKaTile <= sq.nm;
+    if (whole && pieces16) {
+      const uint8_t *k0 = kc + (uint64_t)row0 * Sh::kCodeRow, *k1 = kc + (uint64_t)row1 * Sh::kCodeRow;
+      const uint8_t *v0 = vc + (uint64_t)row0 * Sh::kCodeRow, *v1 = vc + (uint64_t)row1 * Sh::kCodeRow;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tk = tok + 16 * h, left = sq.nm - tk;
-      r0[h] = pg[h] >= 0 ? row_in_page(tk) : 0;
-      mat[h] = (int64_t)max(pg[h], 0) * p.Hkv + kvh;
-      if (pg[h] >= 0 && left > 0) vm |= (left >= 16 ? 0xFFFFu : (1u << left) - 1u) << (16 * h);
+      for (int it = 0; it < ITS; ++it) {
+        const uint32_t ka = D == 256 ? k_at ^ (uint32_t)(it & 1) << 6 : k_at;
+        cp_async16(ka + so + it * 512, (it < HALF ? k0 : k1) + (it % HALF) * 512);
+        cp_async16(v_at + so + it * 512, (it < HALF ? v0 : v1) + (it % HALF) * 512);
+      }
+      const uint32_t sa = ring_u + so + Sh::kKS + lane * 16;
+      if constexpr (NP == 32) {
+        const uint64_t o = (uint64_t)(lane < 16 ? row0 : row1) * Sh::kScaleRow;
+        cp_async16(sa, sc + o);
+        cp_async16(sa + Sh::kVS - Sh::kKS, sc + (p.v.scales - p.k.scales) + o);
+      } else if (lane < 2 * NP) {
+        cp_async16(sa, sc + (uint64_t)(lane % NP < NP / 2 ? row0 : row1) * Sh::kScaleRow);
+      }
+      return;
     }
-    if (lane == 0) vms[w * ST + st] = vm;
-    constexpr int CPR = Sh::kCodeRow / 16, ITS = kKaTile * CPR / 32;   // 16-byte pieces per row, instructions
+    const int n0 = pg0 >= 0 ? min(max(sq.nm - tok, 0), 16) : 0, n1 = pg1 >= 0 ? min(max(sq.nm - tok - 16, 0), 16) : 0;
+    const uint32_t vm = ((1u << n0) - 1u) | ((1u << n1) - 1u) << 16;
+    if (!whole) {
+      partial |= 1u << (i & 31);
+      if (lane == 0) vms[w * ST + st] = vm;
+    }
 #pragma unroll
     for (int it = 0; it < ITS; ++it) {
-      constexpr int HALF = ITS / 2;
-      const int h = it / HALF, row = it * (32 / CPR) + lane / CPR;
-      const int ok = (vm >> row) & 1u;
-      const int64_t off = ok ? (mat[h] * p.page_rows + r0[h]) * Sh::kCodeRow + (it % HALF) * 512 + lane * 16 : 0;
-      const uint32_t at = (uint32_t)(it * 512 + lane * 16);
-      // keys are read as rows r and r + 4 together, values as rows r .. r + 3: each order gets its own
-      // exchange of 64- (32-) byte halves so that both read without bank conflicts
-      const uint32_t ka = at ^ (((uint32_t)row >> 2 & 1u) << 6);
-      const uint32_t va = D == 128 ? at ^ (((uint32_t)row >> 1 & 1u) << 5) : D == 256 ? at ^ (((uint32_t)row & 3u) << 5) : at;
-      cp_async16(dst + Sh::kKC + ka, p.k.codes + off, ok ? 16 : 0);
-      cp_async16(dst + Sh::kVC + va, p.v.codes + off, ok ? 16 : 0);
+      const int ok = vm >> (it * (32 / CPR) + lane_row) & 1u;
+      const uint64_t o = ok ? (uint64_t)(it < HALF ? row0 : row1) * Sh::kCodeRow + (it % HALF) * 512 : 0;
+      const uint32_t ka = D == 256 ? k_at ^ (uint32_t)(it & 1) << 6 : k_at;
+      cp_async16(ka + so + it * 512, kc + o, ok ? 16 : 0);
+      cp_async16(v_at + so + it * 512, vc + o, ok ? 16 : 0);
     }
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      const KvSide& s = side ? p.v : p.k;
-      const uint32_t sd = dst + (side ? Sh::kVS : Sh::kKS);
-      if (s.vec16) {
-        constexpr int RPP = 16 / Sh::kScaleRow, NP = kKaTile / RPP;    // rows per 16 bytes, pieces per tile
-        if (lane < NP) {
-          const int row = lane * RPP, h = row >> 4;
-          const int n = __popc((vm >> row) & ((1u << RPP) - 1u));
-          const int64_t off = n ? (mat[h] * p.page_rows + r0[h] + (row & 15)) * Sh::kScaleRow : 0;
-          cp_async16(sd + row * Sh::kScaleRow, s.scales + off, n * Sh::kScaleRow);
-        }
-      } else {
-        const int h = lane >> 4, ok = (vm >> lane) & 1u, r = r0[h] + (lane & 15);
+      const uint8_t* s = side ? p.v.scales : p.k.scales;
+      const bool tile = side ? p.v.tile : p.k.tile;
+      const int64_t mb = side ? p.v.mat_bytes : p.k.mat_bytes;
+      const uint32_t sd = ring_u + so + (side ? Sh::kVS : Sh::kKS) + lane * Sh::kScaleRow;
+      const int ok = (vm >> lane) & 1u, r = (lane < 16 ? r0 : r1) + (lane & 15);
+      const uint32_t row = (lane < 16 ? row0 : row1) + (lane & 15);
+      const int64_t m = (int64_t)(lane < 16 ? pg0 : pg1) * p.Hkv + kvh;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          int64_t off = 0;
-          if (ok)
-            off = s.tile ? mat[h] * s.mat_bytes + ((int64_t)(r >> 7) * (D / 64) + j) * 512 + 16 * (r & 31) + 4 * (r >> 5 & 3)
-                         : (mat[h] * p.page_rows + r) * Sh::kScaleRow + 4 * j;
-          cp_async4(sd + lane * Sh::kScaleRow + 4 * j, s.scales + off, ok ? 4 : 0);
-        }
+      for (int j = 0; j < D / 64; ++j) {
+        int64_t off = 0;
+        if (ok)
+          off = tile ? m * mb + ((int64_t)(r >> 7) * (D / 64) + j) * 512 + 16 * (r & 31) + 4 * (r >> 5 & 3)
+                     : (int64_t)row * Sh::kScaleRow + 4 * j;
+        cp_async4(sd + 4 * j, s + off, ok ? 4 : 0);
       }
     }
   };
@@ -323,7 +359,7 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
   for (int i = 0; i < ST - 1; ++i) {
     const int a = next[0], c = next[1];
     look_up(i + 1);
-    if (i < n_my) issue(i, a, c);
+    if (i < n_my) issue(i, i, a, c);
     cp_async_commit();
   }
 
@@ -370,6 +406,7 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
       eo[j * 32] = v;
     }
     if (p.k.rotate) fwht16(a);
+    const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;            // carried by the query, so that factors are >= 0
     float mx = 0.0f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(a[k]));
@@ -377,7 +414,7 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
     for (int o = BPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
     int e = (int)(__float_as_uint(mx) >> 23) - 127;                  // floor(log2), exact for normal values
     e = mx > 0.0f && mx <= FLT_MAX ? max(-100, min(100, e)) : 0;
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    const float down = sign * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint4 v;
@@ -388,15 +425,13 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
     if (blk == 0) {
       rowfac[row] = __uint_as_float((uint32_t)(127 + e) << 23);
       // positions this row sees: all before the limit (rows past R restrict nothing and are not written)
-      int64_t lim = sq.len;
-      if (p.causal && r < p.R) lim = max(sq.len - p.Tq + r / p.G + 1, (int64_t)0);
-      limit[row] = (int)min(lim, (int64_t)INT_MAX);
+      limit[row] = p.causal && r < p.R ? max(sq.len - p.Tq + r / p.G + 1, 0) : sq.len;
     }
   }
   __syncthreads();
 
   float O[NO][NT][4], m[NT][2], l[NT][2], fac[NT][2];
-  int lim[NT][2];
+  int lim[NT][2];                               // positions each column's row sees: all before this one
   int lim_min = INT_MAX;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -417,22 +452,26 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
   lim_min = min(lim_min, __shfl_xor_sync(0xFFFFFFFFu, lim_min, 2));
   const int perm = (g >> 1) + 4 * (g & 1);      // the token of fragment row g (row g + 8: + 8)
 
-  // running maximum: raise m to the tile's maxima, rescaling what was summed under the old ones
+  // the tile's tokens (bit k: token k) that a column's row sees
+  auto seen_of = [&](int n, int c, int tok0, uint32_t vm) -> uint32_t {
+    const int rel = max(min(lim[n][c] - sq.ns - tok0, kKaTile), 0);
+    return vm & (rel >= 32 ? 0xFFFFFFFFu : (1u << rel) - 1u);
+  };
+
+  // The reference m of a row's numerators follows its maximum lazily: while no score of the tile passes it by more
+  // than kKaSlack, m and everything summed under it stay (one vote); else m becomes the tile's maximum and the
+  // sums are rescaled.
   auto raise = [&](float (&mx)[NT][2]) {
     bool up = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) up |= mx[n][0] > m[n][0] + kKaSlack || mx[n][1] > m[n][1] + kKaSlack;
+    if (!__any_sync(0xFFFFFFFFu, up)) return;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xFFFFFFFFu, mx[n][c], o));
-        up |= mx[n][c] > m[n][c];
-      }
-    if (!__any_sync(0xFFFFFFFFu, up)) return;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
         const float mn = fmaxf(m[n][c], mx[n][c]);
         const float al = ex2(m[n][c] - finite_or_zero(mn));
         m[n][c] = mn;
@@ -446,36 +485,34 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
   };
 
   if (n_my > 0) {
-    const float gk = p.k.gscale[p.k.gstride * sq.s] * p.scale_log2;
+    const float gk = p.k.gscale[p.k.gstride * sq.s] * fabsf(p.scale_log2);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       fac[n][0] *= gk;
       fac[n][1] *= gk;
     }
   }
+  const int mid_seen = lim_min - sq.ns;         // every row sees the middle's tokens before this one
+  int stage = 0, ahead = ST - 1;                // stages of tile i and of the tile issued with it
   for (int i = 0; i < n_my; ++i) {
     cp_async_wait<ST - 2>();
     __syncwarp();
     {
       const int a = next[0], c = next[1], k = i + ST - 1;
       look_up(k + 1);
-      if (k < n_my) issue(k, a, c);
+      if (k < n_my) issue(k, ahead, a, c);
       cp_async_commit();
     }
-    const unsigned char* st = ring + (i % ST) * Sh::kStageBytes;
-    const uint32_t vm = vms[w * ST + i % ST];
+    const unsigned char* st = ring + stage * Sh::kStageBytes;
     const int tok0 = (t_first + i * kKaWarps) * kKaTile;
-    const int64_t pos0 = (int64_t)sq.ns + tok0;
-    const bool full = vm == 0xFFFFFFFFu && pos0 + kKaTile <= lim_min;
+    const uint32_t vm = partial >> (i & 31) & 1u ? vms[w * ST + stage] : 0xFFFFFFFFu;
+    partial &= ~(1u << (i & 31));
+    stage = stage == ST - 1 ? 0 : stage + 1;
+    ahead = ahead == ST - 1 ? 0 : ahead + 1;
+    const bool full = vm == 0xFFFFFFFFu && tok0 + kKaTile <= mid_seen;
 
     // ---- S^T = K Q^T: rows are tokens (two tiles of 16), columns query rows ----
     float S[2][NT][4];
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) S[a][n][c] = 0.0f;
 #pragma unroll
     for (int cc = 0; cc < KCH; ++cc) {
       uint32_t kw[4][KW], ks[4][KW / 2];         // rows perm + 8 k of the tile; scales doubled into both halves
@@ -487,13 +524,12 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
           const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kKC + ((row * Sh::kCodeRow + (t + 4 * cc) * 16) ^ sw));
           kw[k][0] = v.x, kw[k][1] = v.y, kw[k][2] = v.z, kw[k][3] = v.w;
           const uint32_t h = e4m3x2_f16x2(*reinterpret_cast<const unsigned short*>(st + Sh::kKS + row * Sh::kScaleRow + 2 * t + 8 * cc));
-          ks[k][0] = __byte_perm(h, h, 0x1010);
-          ks[k][1] = __byte_perm(h, h, 0x3232);
+          ks[k][0] = both_lo(h);
+          ks[k][1] = both_hi(h);
         } else {
           const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kKC + ((row * Sh::kCodeRow + t * 8) ^ sw));
           kw[k][0] = v.x, kw[k][1] = v.y;
-          const uint32_t h = e4m3x2_f16x2(st[Sh::kKS + row * Sh::kScaleRow + t]);
-          ks[k][0] = __byte_perm(h, h, 0x1010);
+          ks[k][0] = both_lo(e4m3x2_f16x2(st[Sh::kKS + row * Sh::kScaleRow + t]));
         }
       }
 #pragma unroll
@@ -513,42 +549,44 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
             const uint4 qv = qf[(n * NS + j) * 32 + lane];
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-              mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
+              if (j == 0) mma16816_zero(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
+              else mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
               mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.z, qv.w);
             }
           }
         }
       }
     }
-    // ---- numerators ----
+    // ---- numerators (fac >= 0: maxima are taken before it is applied) ----
     float mx[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        mx[n][c] = -INFINITY;
-        const int rel = (int)max(min((int64_t)lim[n][c] - pos0, (int64_t)kKaTile), (int64_t)0);
-        const uint32_t seen = full ? 0xFFFFFFFFu : vm & (rel >= 32 ? 0xFFFFFFFFu : (1u << rel) - 1u);
+        if (!full) {
+          const uint32_t seen = seen_of(n, c, tok0, vm);
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+          for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float& s = S[a][n][c + 2 * h];
-            s *= fac[n][c];
-            if (!full) s = (seen >> (16 * a + 8 * h + perm)) & 1u ? s : -INFINITY;
-            mx[n][c] = fmaxf(mx[n][c], s);
-          }
+            for (int h = 0; h < 2; ++h)
+              if (!(seen >> (16 * a + 8 * h + perm) & 1u)) S[a][n][c + 2 * h] = -INFINITY;
+        }
+        mx[n][c] = fac[n][c] * fmaxf(fmaxf(S[0][n][c], S[0][n][c + 2]), fmaxf(S[1][n][c], S[1][n][c + 2]));
       }
     raise(mx);
     uint32_t pb[2][NT][2];                       // the second product's B fragments (tokens x query rows)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float s0 = finite_or_zero(m[n][0]) - kKaPShift, s1 = finite_or_zero(m[n][1]) - kKaPShift;
+      const float s0 = kKaPShift - finite_or_zero(m[n][0]), s1 = kKaPShift - finite_or_zero(m[n][1]);
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float p0 = ex2(S[a][n][2 * h] - s0), p1 = ex2(S[a][n][2 * h + 1] - s1);
+          float p0 = ex2(fmaf(S[a][n][2 * h], fac[n][0], s0)), p1 = ex2(fmaf(S[a][n][2 * h + 1], fac[n][1], s1));
+          if (!full) {                           // -Inf times a zero factor would be NaN
+            p0 = S[a][n][2 * h] == -INFINITY ? 0.0f : p0;
+            p1 = S[a][n][2 * h + 1] == -INFINITY ? 0.0f : p1;
+          }
           l[n][0] += p0;
           l[n][1] += p1;
           pb[a][n][h] = movmatrix(pack_f16(p0, p1));
@@ -630,9 +668,7 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const int rel = (int)max(min((int64_t)lim[n][c] - pos0, (int64_t)kKaTile), (int64_t)0);
-                const uint32_t seen = vm & (rel >= 32 ? 0xFFFFFFFFu : (1u << rel) - 1u);
-                if (nan_tok[vb] & seen) {
+                if (nan_tok[vb] & seen_of(n, c, tok0, vm)) {
 #pragma unroll
                   for (int k = 0; k < NO / VB; ++k) O[vb * (NO / VB) + k][n][c] = O[vb * (NO / VB) + k][n][c + 2] = NAN;
                 }
@@ -644,7 +680,7 @@ __global__ void __launch_bounds__(kKaWarps * 32) kv_attn_kernel(const __grid_con
 
   // ---- the middle's sums: undo the numerators' scale, apply g_v, turn back along the channels ----
   if (n_my > 0) {
-    constexpr float kUndo = 1.0f / 32768.0f;
+    constexpr float kUndo = 1.0f / 1024.0f;
     const float gv = p.v.gscale[p.v.gstride * sq.s] * kUndo;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
