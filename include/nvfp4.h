@@ -434,10 +434,11 @@ typedef struct nvfp4_kv_attention_desc {
  * query is carried in 22 bits and its numerators in FP16 (scaled by 2^10), the BF16 ends' in 16 bits.
  * Hidden tokens (past a row's position, past a sequence's end) reach no row, whatever they hold; a visible
  * NaN reaches the rows that see it.
- * splits: 1 .. 128 ranges of the middle per sequence, worked on by different CTAs and then joined by a second
- * kernel (nvfp4_kv_attention_splits gives a count that fills the current device; any count gives a valid
- * result, which depends on it in the last bits).  workspace: caller-owned device memory, 16-byte aligned, of
- * nvfp4_kv_attention_workspace_bytes (NULL with splits == 1); calls that share one must be ordered.
+ * splits: the number of parts (1 .. 65535), one per CTA, that all the call's tokens are cut into evenly, whatever the
+ * lengths; sequences that a cut falls into are joined by a second kernel (nvfp4_kv_attention_splits gives the
+ * count that fills the current device once; any count gives a valid result, which depends on it in the last
+ * bits).  workspace: caller-owned device memory, 16-byte aligned, of nvfp4_kv_attention_workspace_bytes (NULL with
+ * splits == 1); calls that share one must be ordered.
  * No device memory is allocated and no state kept; lengths, slots and table are read on the device, so a
  * captured call follows their contents.  Tensor scales are not negative.  Each part of a sequence holds at most
  * 2^29 - 1 tokens and pages * Hkv * page_rows is below 2^32.  NVFP4_ERR_SIZE for unsupported sizes, NVFP4_ERR_ARG for host lengths
@@ -445,13 +446,13 @@ typedef struct nvfp4_kv_attention_desc {
 int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* workspace, size_t workspace_bytes,
                        void* stream);
 
-/* The number of ranges for nvfp4_kv_attention that fills the current device: rows = (Hq / Hkv) * Tq, max_mid an
- * upper bound on the middle's length (a longer sequence stays correct).  Host only (queries the device). */
+/* The number of parts for nvfp4_kv_attention that fills the current device: rows = (Hq / Hkv) * Tq, max_mid the
+ * longest middle expected (it only sizes the cut).  Host only (queries the device). */
 int nvfp4_kv_attention_splits(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t max_mid, int* splits);
 
-/* Bytes of workspace: B * Hkv * rows * splits FP32 accumulators of D channels and two statistics; 0 for one range
- * or invalid arguments.  Host only. */
-size_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int splits);
+/* Bytes of workspace: per part the FP32 sums of two tiles of 8 (or 16, when rows > 8) query rows of D channels, two
+ * statistics per row and 16 bytes; 0 for one part or invalid arguments.  Host only. */
+size_t nvfp4_kv_attention_workspace_bytes(int64_t rows, int64_t D, int splits);
 
 /* One tensor of a rotary call: x and out [B, heads, T, D] at the given strides (elements; channels contiguous).
  * out may be x itself (the same strides, NVFP4_ERR_ARG otherwise) but must not overlap any x otherwise. */

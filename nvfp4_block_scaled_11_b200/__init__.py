@@ -69,7 +69,7 @@ _SIGS = {
     "nvfp4_attention_fused_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I]),
     "nvfp4_kv_attention": (_I, [_P, _I, _P, ctypes.c_size_t, _P]),
     "nvfp4_kv_attention_splits": (_I, [_I64, _I64, _I64, _I64, _I64, _P]),
-    "nvfp4_kv_attention_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I]),
+    "nvfp4_kv_attention_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I]),
     "nvfp4_rope": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I, _I, _P, _I, _I64, _I64, _P, ctypes.c_float, _I, _P]),
     "nvfp4_copy_pages": (_I, [_P, _I, _P, _P, _I64, _P]),
     "nvfp4_gemm_sf_offsets": (_I, [_I64, _I64, _I64, _P]),
@@ -861,7 +861,7 @@ def _kv_splits(device: torch.device, B: int, H: int, rows: int, D: int, max_mid:
             _check(lib().nvfp4_kv_attention_splits(B, H, rows, D, max_mid, ctypes.byref(s)))
         if len(_kv_splits_memo) > 4096:
             _kv_splits_memo.clear()
-        got = _kv_splits_memo[key] = (s.value, lib().nvfp4_kv_attention_workspace_bytes(B, H, rows, D, s.value))
+        got = _kv_splits_memo[key] = (s.value, lib().nvfp4_kv_attention_workspace_bytes(rows, D, s.value))
     return got
 
 
@@ -944,7 +944,7 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
         splits, need = _kv_splits(dev, B, k.H, rows, D, max(hint, 0))
     else:
         splits = int(splits)
-        need = lib().nvfp4_kv_attention_workspace_bytes(B, k.H, rows, D, splits)
+        need = lib().nvfp4_kv_attention_workspace_bytes(rows, D, splits)
     if workspace is None:
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)

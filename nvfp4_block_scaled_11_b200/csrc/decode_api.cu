@@ -35,23 +35,23 @@ int raise_smem(int bytes) {
 }
 
 template <int D, int NT, bool QBF>
-int launch_kv_attention(const KvAttnParams& p, unsigned grid, unsigned rows, cudaStream_t s) {
+int launch_kv_attention(const KvAttnParams& p, unsigned parts, bool join, cudaStream_t s) {
   constexpr int smem = KaSmem<D, NT>::kBytes;
   if (int rc = raise_smem<kv_attn_kernel<D, NT, QBF>>(smem)) return rc;
-  kv_attn_kernel<D, NT, QBF><<<grid, kKaWarps * 32, smem, s>>>(p);
+  kv_attn_kernel<D, NT, QBF><<<parts, kKaWarps * 32, smem, s>>>(p);
   if (int rc = last_error()) return rc;
-  if (p.nch > 1) {
+  if (join) {
     // launched while the first kernel drains; it waits for that kernel's results itself
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(rows);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(parts, 8 * NT);
+    cfg.blockDim = dim3(kKaJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, QBF>, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, NT, QBF>, p) != cudaSuccess) {
       cudaGetLastError();
       return NVFP4_ERR_CUDA;
     }
@@ -60,14 +60,17 @@ int launch_kv_attention(const KvAttnParams& p, unsigned grid, unsigned rows, cud
 }
 
 template <int D>
-int launch_kv_attention_d(const KvAttnParams& p, bool bf, int nt, unsigned grid, unsigned rows, cudaStream_t s) {
-  if (nt == 1) return bf ? launch_kv_attention<D, 1, true>(p, grid, rows, s) : launch_kv_attention<D, 1, false>(p, grid, rows, s);
-  return bf ? launch_kv_attention<D, 2, true>(p, grid, rows, s) : launch_kv_attention<D, 2, false>(p, grid, rows, s);
+int launch_kv_attention_d(const KvAttnParams& p, bool bf, int nt, unsigned parts, bool join, cudaStream_t s) {
+  if (nt == 1) return bf ? launch_kv_attention<D, 1, true>(p, parts, join, s) : launch_kv_attention<D, 1, false>(p, parts, join, s);
+  return bf ? launch_kv_attention<D, 2, true>(p, parts, join, s) : launch_kv_attention<D, 2, false>(p, parts, join, s);
 }
 
 // Query rows of a CTA in units of 8: one K/V head's rows fit 8 for most decode steps; more rows share the
 // expansion of the codes in tiles of 16.
 int ka_row_units(int64_t rows) { return rows <= 8 ? 1 : 2; }
+
+// CTAs of the attention kernel that an SM holds (its launch bounds and shared memory).
+int ka_ctas_per_sm(int64_t D, int nt) { return D == 256 ? 2 : D == 128 ? (nt == 1 ? 4 : 3) : (nt == 1 ? 5 : 4); }
 
 // One side of the cache: pointers and layout into the kernel's form.
 int ka_side(const nvfp4_kv_store& c, const nvfp4_kv_attention_desc& d, int64_t mid_rows, KvSide& o) {
@@ -101,23 +104,23 @@ extern "C" {
 int nvfp4_kv_attention_splits(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t max_mid, int* splits) {
   if (splits == nullptr) return NVFP4_ERR_ARG;
   if (B < 0 || Hkv < 0 || rows < 0 || max_mid < 0 || max_mid > kMaxInt || (D != 64 && D != 128 && D != 256) ||
-      checked_prod({B, Hkv, rows, D, kKaMaxSplits, 4}) < 0)
+      checked_prod({B, Hkv, rows}) < 0)
     return NVFP4_ERR_SIZE;
   *splits = 1;
   const int nt = ka_row_units(rows);
-  const int64_t base = B * Hkv * ((rows + 8 * nt - 1) / (8 * nt)), tiles = (max_mid + kKaTile - 1) / kKaTile;
-  if (base == 0 || tiles <= kKaMinTiles) return NVFP4_OK;
-  const int64_t slots = (int64_t)sm_count() * (D == 256 ? 2 : nt == 2 ? 3 : 4);
-  const int64_t want = std::max<int64_t>(1, (2 * slots + base - 1) / base);
-  *splits = (int)std::min<int64_t>({want, (tiles + kKaMinTiles - 1) / kKaMinTiles, (int64_t)kKaMaxSplits});
+  const int64_t jobs = checked_prod({B, Hkv, (rows + 8 * nt - 1) / (8 * nt)});
+  const int64_t units = (max_mid + kKaTile * kKaWarps - 1) / (kKaTile * kKaWarps) + 1 + kKaJobUnits;   // of a job, ends of up to 4 tiles
+  const int64_t slots = (int64_t)sm_count() * ka_ctas_per_sm(D, nt);
+  const int64_t work = checked_prod({jobs, units});
+  if (jobs <= 0 || work < 0) return NVFP4_OK;
+  // short jobs (up to 4 units of work) that leave room for all of them at once keep a CTA each: nothing to join
+  *splits = (int)(units <= 4 + kKaJobUnits && jobs <= slots ? jobs : std::min(slots, std::max<int64_t>(work / kKaMinUnits, 1)));
   return NVFP4_OK;
 }
 
-size_t nvfp4_kv_attention_workspace_bytes(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int splits) {
-  if (splits <= 1 || splits > kKaMaxSplits || B < 0 || Hkv < 0 || rows < 0 || D <= 0 ||
-      checked_prod({B, Hkv, rows, D + 2, splits, 4}) < 0)
-    return 0;
-  return (size_t)(B * Hkv * rows * (D + 2) * splits * 4);
+size_t nvfp4_kv_attention_workspace_bytes(int64_t rows, int64_t D, int splits) {
+  if (splits <= 1 || splits > kKaMaxSplits || rows <= 0 || D <= 0 || D > 256) return 0;
+  return (size_t)splits * (2 * 8 * ka_row_units(rows) * (D + 2) * 4 + 16);
 }
 
 int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* workspace, size_t workspace_bytes,
@@ -163,13 +166,11 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* wo
   const int64_t G = d.Hq / d.Hkv, R = checked_prod({G, d.Tq});
   if (R < 0 || R > kMaxInt) return NVFP4_ERR_SIZE;
   const int nt = ka_row_units(R);
-  const int64_t row_tiles = (R + 8 * nt - 1) / (8 * nt);
-  const int64_t grid = checked_prod({d.B, d.Hkv, row_tiles, splits}), rows = checked_prod({d.B, d.Hkv, R});
-  if (grid < 0 || grid > kMaxInt || rows < 0 || rows > kMaxInt || checked_prod({rows, d.D + 2, splits, 4}) < 0)
-    return NVFP4_ERR_SIZE;
+  const int64_t row_tiles = (R + 8 * nt - 1) / (8 * nt), jobs = checked_prod({d.B, d.Hkv, row_tiles});
+  if (jobs < 0 || jobs > kMaxInt) return NVFP4_ERR_SIZE;
   if (splits > 1) {
     if (workspace == nullptr) return NVFP4_ERR_ARG;
-    if (workspace_bytes < nvfp4_kv_attention_workspace_bytes(d.B, d.Hkv, R, d.D, splits)) return NVFP4_ERR_SIZE;
+    if (workspace_bytes < nvfp4_kv_attention_workspace_bytes(R, d.D, splits)) return NVFP4_ERR_SIZE;
   }
   p.q = static_cast<const char*>(d.q);
   p.out = static_cast<char*>(d.out);
@@ -183,17 +184,21 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* wo
   p.slots = d.slots, p.pages = d.pages, p.cols = d.table_cols;
   p.slot = d.slot, p.table = d.table, p.lens = d.lens;
   p.host_lens[0] = d.n_sink, p.host_lens[1] = d.n_mid, p.host_lens[2] = d.head, p.host_lens[3] = d.n_window;
-  p.nch = splits;
+  p.B = (int)d.B;
   p.causal = d.causal;
   p.q_vec = aligned(d.q, 16) && d.q_sb % 8 == 0 && d.q_sh % 8 == 0 && d.q_st % 8 == 0;
   p.scale_log2 = d.scale * 1.4426950408889634f;
-  p.ws_o = static_cast<float*>(workspace);
-  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + (splits > 1 ? rows * splits * d.D : 0));
+  const int64_t ws_rows = (int64_t)splits * 2 * 8 * nt;
+  p.ws_meta = static_cast<int4*>(workspace);
+  p.ws_o = reinterpret_cast<float*>(p.ws_meta + splits);
+  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + ws_rows * d.D);
+  // sequences that are all alike and parts that hold whole jobs: no cut inside a job
+  const bool join = splits > 1 && !(d.lens == nullptr && d.slot == nullptr && jobs % splits == 0);
   const bool bf = d.dtype == NVFP4_BF16;
   cudaStream_t s = S(stream);
-  if (d.D == 64) return launch_kv_attention_d<64>(p, bf, nt, (unsigned)grid, (unsigned)rows, s);
-  if (d.D == 128) return launch_kv_attention_d<128>(p, bf, nt, (unsigned)grid, (unsigned)rows, s);
-  return launch_kv_attention_d<256>(p, bf, nt, (unsigned)grid, (unsigned)rows, s);
+  if (d.D == 64) return launch_kv_attention_d<64>(p, bf, nt, (unsigned)splits, join, s);
+  if (d.D == 128) return launch_kv_attention_d<128>(p, bf, nt, (unsigned)splits, join, s);
+  return launch_kv_attention_d<256>(p, bf, nt, (unsigned)splits, join, s);
 }
 
 int nvfp4_rope(const nvfp4_rope_tensor* tensors, int count, int64_t B, int64_t T, int64_t D, int64_t rot, int interleaved,

@@ -32,14 +32,18 @@
 #include <limits.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "device.cuh"
 
 namespace nvfp4 {
 
 constexpr int kKaWarps = 4;            // warps per CTA, each with its own tiles
 constexpr int kKaTile = 32;            // middle tokens per tile
-constexpr int kKaMinTiles = 8;         // least tiles per range: shorter ones cost more in joining than they win
-constexpr int kKaMaxSplits = 128;
+constexpr int kKaJobUnits = 3;         // what starting and ending a job costs, in units of work (4 tiles)
+constexpr int kKaMinUnits = 4;         // least units per part: shorter ones cost more in joining than they win
+constexpr int kKaMaxSplits = 65535;
+constexpr int kKaJoinWarps = 8;        // warps that join the pieces of one query row
 constexpr float kKaPShift = 10.0f;     // numerators of the middle are scaled by 2^10 before FP16
 constexpr float kKaSlack = 5.0f;       // how far (base 2) a score may pass its row's reference: 2^15 fits FP16
 
@@ -67,10 +71,11 @@ struct KvAttnParams {
   const int32_t* table;    // [slots, cols] or null: slot s is page s
   const int32_t* lens;     // [slots, 4] (n_sink, n_mid, head, n_window) or null: host_lens for every slot
   int host_lens[4];
-  int nch, causal, q_vec;
+  int B, causal, q_vec;
   float scale_log2;        // scale * log2(e)
-  float* ws_o;             // [B Hkv R, nch, D]
-  float2* ws_ml;           // [B Hkv R, nch] maxima (base 2) and sums
+  float* ws_o;             // [parts, 2, rows, D] sums of the jobs that a part shares with the part before / after it
+  float2* ws_ml;           // [parts, 2, rows] their references (base 2) and denominators
+  int4* ws_meta;           // [parts] the job that a part's start cuts first: sequence, head and row tile, parts, flag
 };
 
 template <int D>
@@ -152,6 +157,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// bits of a where m is set, of b elsewhere, in one operation
+__device__ __forceinline__ uint32_t pick(uint32_t a, uint32_t b, uint32_t m) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(a), "r"(b), "r"(m));
+  return r;
+}
 __device__ __forceinline__ uint32_t both_lo(uint32_t h) {
   uint32_t r;
   asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; mov.b32 %0, {a, a}; }" : "=r"(r) : "r"(h));
@@ -216,12 +227,29 @@ __device__ __forceinline__ KaSeq ka_sequence(const KvAttnParams& p, int b) {
   q.len = q.ns + q.nm + q.nw;
   return q;
 }
-// Tiles per range and the ranges that hold any (at least one) of a middle of nm tokens.
-__device__ __forceinline__ void ka_ranges(int nm, int nch, int& per, int& active) {
-  const int tiles = (nm + kKaTile - 1) / kKaTile;
-  per = max((tiles + nch - 1) / nch, kKaMinTiles);
-  active = max((tiles + per - 1) / per, 1);
+// The call's work in units: of a job (a sequence, K/V head and tile of query rows) kKaJobUnits for starting and ending
+// it, then one per 4 tiles of the middle (a tile per warp) and one per 4 tiles of the BF16 ends, at least one.
+// Units are numbered job after job and cut into equal parts, one per CTA: whatever the lengths, the CTAs do the same
+// work in one wave, and only the jobs that a cut falls into have to be joined.  A cut among a job's first
+// kKaJobUnits units moves to its beginning.
+__device__ __forceinline__ int ka_mid_units(const KaSeq& q) { return (q.nm + kKaTile * kKaWarps - 1) / (kKaTile * kKaWarps); }
+__device__ __forceinline__ int ka_end_tiles(const KaSeq& q) { return (q.ns + 15) / 16 + (q.nw + 15) / 16; }
+__device__ __forceinline__ int ka_units(const KaSeq& q) {
+  return kKaJobUnits + max(ka_mid_units(q) + (ka_end_tiles(q) + kKaWarps - 1) / kKaWarps, 1);
 }
+struct KaParts {
+  int64_t base, rem;                    // part c starts at c base + min(c, rem)
+  int n;
+  __device__ __forceinline__ KaParts(int64_t total, int most) {
+    n = (int)min((int64_t)most, max(total / kKaMinUnits, (int64_t)1));
+    base = total / n;
+    rem = total - base * n;
+  }
+  __device__ __forceinline__ int64_t start(int c) const { return c * base + min((int64_t)c, rem); }
+  __device__ __forceinline__ int of(int64_t u) const {
+    return (int)(u < rem * (base + 1) ? u / (base + 1) : rem + (u - rem * (base + 1)) / base);
+  }
+};
 
 template <bool BF>
 __device__ __forceinline__ void ka_store(char* out, int64_t i, float x) {
@@ -231,7 +259,8 @@ __device__ __forceinline__ void ka_store(char* out, int64_t i, float x) {
 
 // D: head_dim; NT: query rows / 8 of a CTA; QBF: q and out are BF16 (else FP16).
 template <int D, int NT, bool QBF>
-__global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? (NT == 1 ? 3 : 2) : D == 128 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 5 : 4)) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 5 : 4))
+    kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
   using Sh = KaShape<D>;
   using Sm = KaSmem<D, NT>;
   constexpr int ST = Sh::kStages, NS = D / 16 /* k16 steps */, NO = D / 16 /* m16 tiles of channels */;
@@ -246,695 +275,781 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? (NT == 1 ? 3 : 2) : 
   float* rowfac = reinterpret_cast<float*>(smem + Sm::kRing + 2 * Sm::kQ + Sm::kStat);
   int* limit = reinterpret_cast<int*>(rowfac + ROWS);
   uint32_t* vms = reinterpret_cast<uint32_t*>(limit + ROWS);         // [warp][stage]: the tile's tokens that exist
+  __shared__ int64_t scan[kKaWarps + 1];
+  __shared__ int found_b;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
-  int x = blockIdx.x;
-  const int row_tile = x % p.row_tiles;
-  x /= p.row_tiles;
-  const int ch = x % p.nch;
-  x /= p.nch;
-  const int kvh = x % p.Hkv, b = x / p.Hkv;
-  const KaSeq sq = ka_sequence(p, b);
-  int per, active;
-  ka_ranges(sq.nm, p.nch, per, active);
-  if (ch >= active) return;
-  const int tiles = (sq.nm + kKaTile - 1) / kKaTile;
-  const int t_first = ch * per + w, t_end = min(tiles, (ch + 1) * per);
-  const int n_my = t_first < t_end ? (t_end - t_first + kKaWarps - 1) / kKaWarps : 0;
+  const int part = blockIdx.x, jobs_per_seq = p.Hkv * p.row_tiles;
 
-  // ---- the warp's ring: tile i of this warp goes to stage i % ST ----
-  unsigned char* ring = smem + w * ST * Sh::kStageBytes;
-  const uint32_t ring_u = smem_u32(ring);
-  // Rows of the middle are numbered page by page (below 2^32, checked on the host): row (page Hkv + head) page_rows +
-  // r.  Keys are read as rows r and r + 4 together, values as rows r .. r + 3: each order gets its own exchange of
-  // 64- (32-) byte halves in shared memory so that both read without bank conflicts; a lane's exchange is the
-  // same in every instruction but for D = 256 keys.
-  constexpr int CPR = Sh::kCodeRow / 16, ITS = kKaTile * CPR / 32, HALF = ITS / 2;   // pieces per row, instructions
-  const uint32_t lane_row = lane / CPR;
-  const uint32_t k_at = ring_u + Sh::kKC + (lane * 16 ^ (D == 256 ? 0u : (lane_row >> 2 & 1u) << 6));
-  const uint32_t v_at = ring_u + Sh::kVC + (D == 128 ? lane * 16 ^ (lane_row >> 1 & 1u) << 5 : D == 256 ? lane * 16 ^ (lane_row & 3u) << 5 : lane * 16);
-  const uint8_t* kc = p.k.codes + lane * 16;
-  const uint8_t* vc = p.v.codes + lane * 16;
-  constexpr int RPP = 16 / Sh::kScaleRow, NP = kKaTile / RPP;        // scale rows per 16 bytes, pieces per tile and side
-  const uint8_t* sc = (NP == 32 || lane < NP ? p.k.scales : p.v.scales) + lane % (NP / 2) * 16;   // NP < 32: keys', then values'
-  const bool pieces16 = p.k.vec16 && p.v.vec16;
-  const uint32_t head_rows = (uint32_t)p.Hkv * (uint32_t)p.page_rows, my_rows = (uint32_t)kvh * (uint32_t)p.page_rows;
-  const int32_t* my_table = p.table ? p.table + (int64_t)sq.s * p.cols : nullptr;
-  const int mask = p.page_shift >= 0 ? p.page_rows - 1 : 0;
-  auto page_of = [&](int tok) -> int {          // the page holding middle token tok, -1: none
-    if (tok >= sq.nm) return -1;
-    if (!my_table) return sq.s;
-    const int pg = __ldg(my_table + (p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_rows));
-    return (uint32_t)pg < (uint32_t)p.pages ? pg : -1;
-  };
-  auto row_in_page = [&](int tok) -> int { return !my_table ? tok : p.page_shift >= 0 ? tok & mask : tok % p.page_rows; };
-  uint32_t partial = 0;                         // bit i % 32: tile i does not hold 32 tokens (which it holds: vms)
-  auto issue = [&](int i, int st, int pg0, int pg1) {
-    const int tok = (t_first + i * kKaWarps) * kKaTile;
-    const uint32_t so = st * Sh::kStageBytes;
-    const int r0 = row_in_page(tok), r1 = row_in_page(tok + 16);
-    const uint32_t row0 = (uint32_t)pg0 * head_rows + my_rows + r0, row1 = (uint32_t)pg1 * head_rows + my_rows + r1;
-    const bool whole = (pg0 | pg1) >= 0 && tok + kKaTile <= sq.nm;
-    if (whole && pieces16) {
-      const uint8_t *k0 = kc + (uint64_t)row0 * Sh::kCodeRow, *k1 = kc + (uint64_t)row1 * Sh::kCodeRow;
-      const uint8_t *v0 = vc + (uint64_t)row0 * Sh::kCodeRow, *v1 = vc + (uint64_t)row1 * Sh::kCodeRow;
+  // ---- this CTA's units, and the sequence that holds the first ----
+  int64_t total, seq_start;
+  int b;
+  if (p.lens == nullptr && p.slot == nullptr) {                       // all sequences alike
+    const int64_t per_seq = (int64_t)ka_units(ka_sequence(p, 0)) * jobs_per_seq;
+    total = per_seq * p.B;
+    const KaParts parts(total, gridDim.x);
+    b = part < parts.n ? (int)(parts.start(part) / per_seq) : 0;
+    seq_start = b * per_seq;
+  } else {
+    const int each = (p.B + kKaWarps * 32 - 1) / (kKaWarps * 32), b0 = min(tid * each, p.B), b1 = min(b0 + each, p.B);
+    int64_t sum = 0;
+    for (int i = b0; i < b1; ++i) sum += (int64_t)ka_units(ka_sequence(p, i)) * jobs_per_seq;
+    int64_t upto = sum;                                               // inclusive prefix over the CTA's threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[w] = upto;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kKaWarps; ++i) {
+      if (i < w) upto += scan[i];
+      total += scan[i];
+    }
+    __syncthreads();                                                  // scan is written again below
+    const KaParts parts(total, gridDim.x);
+    const int64_t u0 = part < parts.n ? parts.start(part) : total;
+    int64_t at = upto - sum;
+    if (u0 >= at && u0 < upto) {
+      int i = b0;
+      for (;; ++i) {
+        const int64_t n = (int64_t)ka_units(ka_sequence(p, i)) * jobs_per_seq;
+        if (u0 < at + n) break;
+        at += n;
+      }
+      scan[0] = at;
+      found_b = i;
+    }
+    __syncthreads();
+    seq_start = scan[0];
+    b = found_b;
+  }
+  const KaParts parts(total, gridDim.x);
+  if (part >= parts.n) {
+    if (gridDim.x > 1 && tid == 0) p.ws_meta[part] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  int64_t u = parts.start(part);
+  const int64_t u_end = parts.start(part + 1);
+  KaSeq sq = ka_sequence(p, b);
+  int cost = ka_units(sq);
+  if (gridDim.x > 1 && tid == 0) {
+    const int64_t in_seq = u - seq_start, job = in_seq / cost, s = seq_start + job * cost + kKaJobUnits;
+    const bool first = s < u && parts.start(part - 1) <= s;           // the first cut inside its job joins it
+    p.ws_meta[part] = first ? make_int4(b, (int)job, parts.of(s - kKaJobUnits + cost - 1) - part + 2, 1) : make_int4(0, 0, 0, 0);
+  }
+
+  while (u < u_end) {
+    if (u - seq_start >= (int64_t)cost * jobs_per_seq) {
+      seq_start += (int64_t)cost * jobs_per_seq;
+      sq = ka_sequence(p, ++b);
+      cost = ka_units(sq);
+    }
+    const int job = (int)((u - seq_start) / cost), units = cost - kKaJobUnits;
+    const int64_t job_work = seq_start + (int64_t)job * cost + kKaJobUnits;
+    if (u_end <= job_work) break;                                     // the next part begins the job
+    const int first_unit = (int)max(u - job_work, (int64_t)0), last_unit = (int)min((int64_t)units, u_end - job_work);
+    u = job_work + units;
+    const int kvh = job / p.row_tiles, row_tile = job - kvh * p.row_tiles;
+    const int mid_units = ka_mid_units(sq), tiles = (sq.nm + kKaTile - 1) / kKaTile;
+    const int t_first = min(first_unit, mid_units) * kKaWarps + w, t_end = min(tiles, min(last_unit, mid_units) * kKaWarps);
+    const int n_my = t_first < t_end ? (t_end - t_first + kKaWarps - 1) / kKaWarps : 0;
+
+    // ---- the warp's ring: tile i of this warp goes to stage i % ST ----
+    unsigned char* ring = smem + w * ST * Sh::kStageBytes;
+    const uint32_t ring_u = smem_u32(ring);
+    // Rows of the middle are numbered page by page (below 2^32, checked on the host): row (page Hkv + head) page_rows +
+    // r.  Keys are read as rows r and r + 4 together, values as rows r .. r + 3: each order gets its own exchange of
+    // 64- (32-) byte halves in shared memory so that both read without bank conflicts; a lane's exchange is the
+    // same in every instruction but for D = 256 keys.
+    constexpr int CPR = Sh::kCodeRow / 16, ITS = kKaTile * CPR / 32, HALF = ITS / 2;   // pieces per row, instructions
+    const uint32_t lane_row = lane / CPR;
+    const uint32_t k_at = ring_u + Sh::kKC + (lane * 16 ^ (D == 256 ? 0u : (lane_row >> 2 & 1u) << 6));
+    const uint32_t v_at = ring_u + Sh::kVC + (D == 128 ? lane * 16 ^ (lane_row >> 1 & 1u) << 5 : D == 256 ? lane * 16 ^ (lane_row & 3u) << 5 : lane * 16);
+    const uint8_t* kc = p.k.codes + lane * 16;
+    const uint8_t* vc = p.v.codes + lane * 16;
+    constexpr int RPP = 16 / Sh::kScaleRow, NP = kKaTile / RPP;        // scale rows per 16 bytes, pieces per tile and side
+    const uint8_t* sc = (NP == 32 || lane < NP ? p.k.scales : p.v.scales) + lane % (NP / 2) * 16;   // NP < 32: keys', then values'
+    const bool pieces16 = p.k.vec16 && p.v.vec16;
+    const uint32_t head_rows = (uint32_t)p.Hkv * (uint32_t)p.page_rows, my_rows = (uint32_t)kvh * (uint32_t)p.page_rows;
+    const int32_t* my_table = p.table ? p.table + (int64_t)sq.s * p.cols : nullptr;
+    const int mask = p.page_shift >= 0 ? p.page_rows - 1 : 0;
+    auto page_of = [&](int tok) -> int {          // the page holding middle token tok, -1: none
+      if (tok >= sq.nm) return -1;
+      if (!my_table) return sq.s;
+      const int pg = __ldg(my_table + (p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_rows));
+      return (uint32_t)pg < (uint32_t)p.pages ? pg : -1;
+    };
+    auto row_in_page = [&](int tok) -> int { return !my_table ? tok : p.page_shift >= 0 ? tok & mask : tok % p.page_rows; };
+    uint32_t partial = 0;                         // bit i % 32: tile i does not hold 32 tokens (which it holds: vms)
+    auto issue = [&](int i, int st, int pg0, int pg1) {
+      const int tok = (t_first + i * kKaWarps) * kKaTile;
+      const uint32_t so = st * Sh::kStageBytes;
+      const int r0 = row_in_page(tok), r1 = row_in_page(tok + 16);
+      const uint32_t row0 = (uint32_t)pg0 * head_rows + my_rows + r0, row1 = (uint32_t)pg1 * head_rows + my_rows + r1;
+      const bool whole = (pg0 | pg1) >= 0 && tok + kKaTile <= sq.nm;
+      if (whole && pieces16) {
+        const uint8_t *k0 = kc + (uint64_t)row0 * Sh::kCodeRow, *k1 = kc + (uint64_t)row1 * Sh::kCodeRow;
+        const uint8_t *v0 = vc + (uint64_t)row0 * Sh::kCodeRow, *v1 = vc + (uint64_t)row1 * Sh::kCodeRow;
+#pragma unroll
+        for (int it = 0; it < ITS; ++it) {
+          const uint32_t ka = D == 256 ? k_at ^ (uint32_t)(it & 1) << 6 : k_at;
+          cp_async16(ka + so + it * 512, (it < HALF ? k0 : k1) + (it % HALF) * 512);
+          cp_async16(v_at + so + it * 512, (it < HALF ? v0 : v1) + (it % HALF) * 512);
+        }
+        const uint32_t sa = ring_u + so + Sh::kKS + lane * 16;
+        if constexpr (NP == 32) {
+          const uint64_t o = (uint64_t)(lane < 16 ? row0 : row1) * Sh::kScaleRow;
+          cp_async16(sa, sc + o);
+          cp_async16(sa + Sh::kVS - Sh::kKS, sc + (p.v.scales - p.k.scales) + o);
+        } else if (lane < 2 * NP) {
+          cp_async16(sa, sc + (uint64_t)(lane % NP < NP / 2 ? row0 : row1) * Sh::kScaleRow);
+        }
+        return;
+      }
+      const int n0 = pg0 >= 0 ? min(max(sq.nm - tok, 0), 16) : 0, n1 = pg1 >= 0 ? min(max(sq.nm - tok - 16, 0), 16) : 0;
+      const uint32_t vm = ((1u << n0) - 1u) | ((1u << n1) - 1u) << 16;
+      if (!whole) {
+        partial |= 1u << (i & 31);
+        if (lane == 0) vms[w * ST + st] = vm;
+      }
 #pragma unroll
       for (int it = 0; it < ITS; ++it) {
+        const int ok = vm >> (it * (32 / CPR) + lane_row) & 1u;
+        const uint64_t o = ok ? (uint64_t)(it < HALF ? row0 : row1) * Sh::kCodeRow + (it % HALF) * 512 : 0;
         const uint32_t ka = D == 256 ? k_at ^ (uint32_t)(it & 1) << 6 : k_at;
-        cp_async16(ka + so + it * 512, (it < HALF ? k0 : k1) + (it % HALF) * 512);
-        cp_async16(v_at + so + it * 512, (it < HALF ? v0 : v1) + (it % HALF) * 512);
+        cp_async16(ka + so + it * 512, kc + o, ok ? 16 : 0);
+        cp_async16(v_at + so + it * 512, vc + o, ok ? 16 : 0);
       }
-      const uint32_t sa = ring_u + so + Sh::kKS + lane * 16;
-      if constexpr (NP == 32) {
-        const uint64_t o = (uint64_t)(lane < 16 ? row0 : row1) * Sh::kScaleRow;
-        cp_async16(sa, sc + o);
-        cp_async16(sa + Sh::kVS - Sh::kKS, sc + (p.v.scales - p.k.scales) + o);
-      } else if (lane < 2 * NP) {
-        cp_async16(sa, sc + (uint64_t)(lane % NP < NP / 2 ? row0 : row1) * Sh::kScaleRow);
-      }
-      return;
-    }
-    const int n0 = pg0 >= 0 ? min(max(sq.nm - tok, 0), 16) : 0, n1 = pg1 >= 0 ? min(max(sq.nm - tok - 16, 0), 16) : 0;
-    const uint32_t vm = ((1u << n0) - 1u) | ((1u << n1) - 1u) << 16;
-    if (!whole) {
-      partial |= 1u << (i & 31);
-      if (lane == 0) vms[w * ST + st] = vm;
-    }
 #pragma unroll
-    for (int it = 0; it < ITS; ++it) {
-      const int ok = vm >> (it * (32 / CPR) + lane_row) & 1u;
-      const uint64_t o = ok ? (uint64_t)(it < HALF ? row0 : row1) * Sh::kCodeRow + (it % HALF) * 512 : 0;
-      const uint32_t ka = D == 256 ? k_at ^ (uint32_t)(it & 1) << 6 : k_at;
-      cp_async16(ka + so + it * 512, kc + o, ok ? 16 : 0);
-      cp_async16(v_at + so + it * 512, vc + o, ok ? 16 : 0);
-    }
+      for (int side = 0; side < 2; ++side) {
+        const uint8_t* s = side ? p.v.scales : p.k.scales;
+        const bool tile = side ? p.v.tile : p.k.tile;
+        const int64_t mb = side ? p.v.mat_bytes : p.k.mat_bytes;
+        const uint32_t sd = ring_u + so + (side ? Sh::kVS : Sh::kKS) + lane * Sh::kScaleRow;
+        const int ok = (vm >> lane) & 1u, r = (lane < 16 ? r0 : r1) + (lane & 15);
+        const uint32_t row = (lane < 16 ? row0 : row1) + (lane & 15);
+        const int64_t m = (int64_t)(lane < 16 ? pg0 : pg1) * p.Hkv + kvh;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const uint8_t* s = side ? p.v.scales : p.k.scales;
-      const bool tile = side ? p.v.tile : p.k.tile;
-      const int64_t mb = side ? p.v.mat_bytes : p.k.mat_bytes;
-      const uint32_t sd = ring_u + so + (side ? Sh::kVS : Sh::kKS) + lane * Sh::kScaleRow;
-      const int ok = (vm >> lane) & 1u, r = (lane < 16 ? r0 : r1) + (lane & 15);
-      const uint32_t row = (lane < 16 ? row0 : row1) + (lane & 15);
-      const int64_t m = (int64_t)(lane < 16 ? pg0 : pg1) * p.Hkv + kvh;
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        int64_t off = 0;
-        if (ok)
-          off = tile ? m * mb + ((int64_t)(r >> 7) * (D / 64) + j) * 512 + 16 * (r & 31) + 4 * (r >> 5 & 3)
-                     : (int64_t)row * Sh::kScaleRow + 4 * j;
-        cp_async4(sd + 4 * j, s + off, ok ? 4 : 0);
-      }
-    }
-  };
-  int next[2];                                  // pages of the tile that is issued next
-  auto look_up = [&](int i) {
-    const int tok = (t_first + i * kKaWarps) * kKaTile;
-    next[0] = i < n_my ? page_of(tok) : -1;
-    next[1] = i < n_my ? page_of(tok + 16) : -1;
-  };
-  look_up(0);
-#pragma unroll
-  for (int i = 0; i < ST - 1; ++i) {
-    const int a = next[0], c = next[1];
-    look_up(i + 1);
-    if (i < n_my) issue(i, i, a, c);
-    cp_async_commit();
-  }
-
-  // ---- the query rows: 16-channel blocks, rotated, scaled by a power of two per row, in fragment order ----
-  constexpr int BPR = D / 16;                   // blocks per row, handled by adjacent lanes
-#pragma unroll
-  for (int u0 = 0; u0 < ROWS * BPR; u0 += kKaWarps * 32) {
-    const int u = u0 + tid;
-    if (ROWS * BPR % (kKaWarps * 32) != 0 && u >= ROWS * BPR) break;   // whole warps leave (ROWS * BPR is a multiple of 32)
-    const int row = u / BPR, blk = u % BPR, r = row_tile * ROWS + row;
-    float a[16];
-    if (r < p.R) {
-      const int i = r / p.G, hq = kvh * p.G + r % p.G;
-      const int64_t at = b * p.q_sb + hq * p.q_sh + i * p.q_st + blk * 16;
-      uint32_t wd[8];
-      if (p.q_vec) {
-        ld_v4(p.q + at * 2, wd);
-        ld_v4(p.q + at * 2 + 16, wd + 4);
-      } else {
-        const unsigned short* s = reinterpret_cast<const unsigned short*>(p.q) + at;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) wd[k] = s[2 * k] | (uint32_t)s[2 * k + 1] << 16;
-      }
-      widen_words<QBF ? DT_BF16 : DT_F16>(wd, a, 8);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) a[k] = 0.0f;
-    }
-    // channel c of the row sits in key chunk c / CD, read by thread t of the fragment; 4 channels per step
-    constexpr int CD = D >= 128 ? 32 : 16;
-    const int c0 = blk * 16, chunk = c0 / CD, ft = chunk & 3, j0 = (chunk >> 2) * 8 + (c0 % CD) / 4;
-    const int fl = (row & 7) * 4 + ft, nt = row >> 3;
-    uint4* eo = qe + (nt * NS + j0) * 32 + fl;
-    uint4* fo = qf + (nt * NS + j0) * 32 + fl;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint4 v;
-      if constexpr (QBF) {
-        v = make_uint4(pack_bf16(a[4 * j], a[4 * j + 1]), pack_bf16(a[4 * j + 2], a[4 * j + 3]), 0u, 0u);
-      } else {
-        split_bf16(a[4 * j], a[4 * j + 1], v.x, v.z);
-        split_bf16(a[4 * j + 2], a[4 * j + 3], v.y, v.w);
-      }
-      eo[j * 32] = v;
-    }
-    if (p.k.rotate) fwht16(a);
-    const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;            // carried by the query, so that factors are >= 0
-    float mx = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(a[k]));
-#pragma unroll
-    for (int o = BPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    int e = (int)(__float_as_uint(mx) >> 23) - 127;                  // floor(log2), exact for normal values
-    e = mx > 0.0f && mx <= FLT_MAX ? max(-100, min(100, e)) : 0;
-    const float down = sign * __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint4 v;
-      split_f16(a[4 * j] * down, a[4 * j + 1] * down, v.x, v.z);
-      split_f16(a[4 * j + 2] * down, a[4 * j + 3] * down, v.y, v.w);
-      fo[j * 32] = v;
-    }
-    if (blk == 0) {
-      rowfac[row] = __uint_as_float((uint32_t)(127 + e) << 23);
-      // positions this row sees: all before the limit (rows past R restrict nothing and are not written)
-      limit[row] = p.causal && r < p.R ? max(sq.len - p.Tq + r / p.G + 1, 0) : sq.len;
-    }
-  }
-  __syncthreads();
-
-  float O[NO][NT][4], m[NT][2], l[NT][2], fac[NT][2];
-  int lim[NT][2];                               // positions each column's row sees: all before this one
-  int lim_min = INT_MAX;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      m[n][c] = -INFINITY;
-      l[n][c] = 0.0f;
-      lim[n][c] = limit[8 * n + 2 * t + c];
-      lim_min = min(lim_min, lim[n][c]);
-      fac[n][c] = rowfac[8 * n + 2 * t + c];
-    }
-#pragma unroll
-    for (int i = 0; i < NO; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) O[i][n][c] = 0.0f;
-  }
-  lim_min = min(lim_min, __shfl_xor_sync(0xFFFFFFFFu, lim_min, 1));
-  lim_min = min(lim_min, __shfl_xor_sync(0xFFFFFFFFu, lim_min, 2));
-  const int perm = (g >> 1) + 4 * (g & 1);      // the token of fragment row g (row g + 8: + 8)
-
-  // the tile's tokens (bit k: token k) that a column's row sees
-  auto seen_of = [&](int n, int c, int tok0, uint32_t vm) -> uint32_t {
-    const int rel = max(min(lim[n][c] - sq.ns - tok0, kKaTile), 0);
-    return vm & (rel >= 32 ? 0xFFFFFFFFu : (1u << rel) - 1u);
-  };
-
-  // The reference m of a row's numerators follows its maximum lazily: while no score of the tile passes it by more
-  // than kKaSlack, m and everything summed under it stay (one vote); else m becomes the tile's maximum and the
-  // sums are rescaled.
-  auto raise = [&](float (&mx)[NT][2]) {
-    bool up = false;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) up |= mx[n][0] > m[n][0] + kKaSlack || mx[n][1] > m[n][1] + kKaSlack;
-    if (!__any_sync(0xFFFFFFFFu, up)) return;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xFFFFFFFFu, mx[n][c], o));
-        const float mn = fmaxf(m[n][c], mx[n][c]);
-        const float al = ex2(m[n][c] - finite_or_zero(mn));
-        m[n][c] = mn;
-        l[n][c] *= al;
-#pragma unroll
-        for (int i = 0; i < NO; ++i) {
-          O[i][n][c] *= al;
-          O[i][n][c + 2] *= al;
+        for (int j = 0; j < D / 64; ++j) {
+          int64_t off = 0;
+          if (ok)
+            off = tile ? m * mb + ((int64_t)(r >> 7) * (D / 64) + j) * 512 + 16 * (r & 31) + 4 * (r >> 5 & 3)
+                       : (int64_t)row * Sh::kScaleRow + 4 * j;
+          cp_async4(sd + 4 * j, s + off, ok ? 4 : 0);
         }
       }
-  };
-
-  if (n_my > 0) {
-    const float gk = p.k.gscale[p.k.gstride * sq.s] * fabsf(p.scale_log2);
+    };
+    int next[2];                                  // pages of the tile that is issued next
+    auto look_up = [&](int i) {
+      const int tok = (t_first + i * kKaWarps) * kKaTile;
+      next[0] = i < n_my ? page_of(tok) : -1;
+      next[1] = i < n_my ? page_of(tok + 16) : -1;
+    };
+    look_up(0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      fac[n][0] *= gk;
-      fac[n][1] *= gk;
-    }
-  }
-  const int mid_seen = lim_min - sq.ns;         // every row sees the middle's tokens before this one
-  int stage = 0, ahead = ST - 1;                // stages of tile i and of the tile issued with it
-  for (int i = 0; i < n_my; ++i) {
-    cp_async_wait<ST - 2>();
-    __syncwarp();
-    {
-      const int a = next[0], c = next[1], k = i + ST - 1;
-      look_up(k + 1);
-      if (k < n_my) issue(k, ahead, a, c);
+    for (int i = 0; i < ST - 1; ++i) {
+      const int a = next[0], c = next[1];
+      look_up(i + 1);
+      if (i < n_my) issue(i, i, a, c);
       cp_async_commit();
     }
-    const unsigned char* st = ring + stage * Sh::kStageBytes;
-    const int tok0 = (t_first + i * kKaWarps) * kKaTile;
-    const uint32_t vm = partial >> (i & 31) & 1u ? vms[w * ST + stage] : 0xFFFFFFFFu;
-    partial &= ~(1u << (i & 31));
-    stage = stage == ST - 1 ? 0 : stage + 1;
-    ahead = ahead == ST - 1 ? 0 : ahead + 1;
-    const bool full = vm == 0xFFFFFFFFu && tok0 + kKaTile <= mid_seen;
 
-    // ---- S^T = K Q^T: rows are tokens (two tiles of 16), columns query rows ----
-    float S[2][NT][4];
+    // the BF16 ends are read last: ask for them now
+    const int sink_tiles = (sq.ns + 15) / 16, e_end = min(ka_end_tiles(sq), (last_unit - mid_units) * kKaWarps);
+    const int e_first = max(first_unit - mid_units, 0) * kKaWarps + w;
+    if (e_first < e_end && n_my > 0) {
+      const int in = e_first < sink_tiles, r = 16 * (in ? e_first : e_first - sink_tiles) + (lane & 15);
+      if (r < (in ? sq.ns : sq.nw)) {
+        const int rows = in ? p.sink_rows : p.window_rows, at = in ? r : r + sq.head >= rows ? r + sq.head - rows : r + sq.head;
+        const KvSide& s = lane < 16 ? p.k : p.v;
+        const char* src = (in ? s.sink : s.window) + (((int64_t)sq.s * p.Hkv + kvh) * rows + at) * (D * 2);
 #pragma unroll
-    for (int cc = 0; cc < KCH; ++cc) {
-      uint32_t kw[4][KW], ks[4][KW / 2];         // rows perm + 8 k of the tile; scales doubled into both halves
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int row = perm + 8 * k;
-        const uint32_t sw = ((uint32_t)row >> 2 & 1u) << 6;
-        if constexpr (KW == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kKC + ((row * Sh::kCodeRow + (t + 4 * cc) * 16) ^ sw));
-          kw[k][0] = v.x, kw[k][1] = v.y, kw[k][2] = v.z, kw[k][3] = v.w;
-          const uint32_t h = e4m3x2_f16x2(*reinterpret_cast<const unsigned short*>(st + Sh::kKS + row * Sh::kScaleRow + 2 * t + 8 * cc));
-          ks[k][0] = both_lo(h);
-          ks[k][1] = both_hi(h);
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kKC + ((row * Sh::kCodeRow + t * 8) ^ sw));
-          kw[k][0] = v.x, kw[k][1] = v.y;
-          ks[k][0] = both_lo(e4m3x2_f16x2(st[Sh::kKS + row * Sh::kScaleRow + t]));
-        }
-      }
-#pragma unroll
-      for (int wd = 0; wd < KW; ++wd) {          // a word of 8 codes feeds two steps
-        uint32_t h[4][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          e2m1x8(kw[k][wd], h[k]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) h[k][c] = hmul2(h[k][c], ks[k][wd >> 1]);
-        }
-#pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) {
-          const int j = cc * 8 + wd * 2 + j2;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 qv = qf[(n * NS + j) * 32 + lane];
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              if (j == 0) mma16816_zero(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
-              else mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
-              mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.z, qv.w);
-            }
-          }
-        }
+        for (int k = 0; k < D * 2; k += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + k));
       }
     }
-    // ---- numerators (fac >= 0: maxima are taken before it is applied) ----
-    float mx[NT][2];
+
+    // ---- the query rows: 16-channel blocks, rotated, scaled by a power of two per row, in fragment order ----
+    constexpr int BPR = D / 16;                   // blocks per row, handled by adjacent lanes
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int i0 = 0; i0 < ROWS * BPR; i0 += kKaWarps * 32) {
+      const int item = i0 + tid;
+      if (ROWS * BPR % (kKaWarps * 32) != 0 && item >= ROWS * BPR) break;   // whole warps leave (ROWS * BPR is a multiple of 32)
+      const int row = item / BPR, blk = item % BPR, r = row_tile * ROWS + row;
+      float a[16];
+      if (r < p.R) {
+        const int i = r / p.G, hq = kvh * p.G + r % p.G;
+        const int64_t at = b * p.q_sb + hq * p.q_sh + i * p.q_st + blk * 16;
+        uint32_t wd[8];
+        if (p.q_vec) {
+          ld_v4(p.q + at * 2, wd);
+          ld_v4(p.q + at * 2 + 16, wd + 4);
+        } else {
+          const unsigned short* s = reinterpret_cast<const unsigned short*>(p.q) + at;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (!full) {
-          const uint32_t seen = seen_of(n, c, tok0, vm);
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (!(seen >> (16 * a + 8 * h + perm) & 1u)) S[a][n][c + 2 * h] = -INFINITY;
+          for (int k = 0; k < 8; ++k) wd[k] = s[2 * k] | (uint32_t)s[2 * k + 1] << 16;
         }
-        mx[n][c] = fac[n][c] * fmaxf(fmaxf(S[0][n][c], S[0][n][c + 2]), fmaxf(S[1][n][c], S[1][n][c + 2]));
+        widen_words<QBF ? DT_BF16 : DT_F16>(wd, a, 8);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) a[k] = 0.0f;
       }
-    raise(mx);
-    uint32_t pb[2][NT][2];                       // the second product's B fragments (tokens x query rows)
+      // channel c of the row sits in key chunk c / CD, read by thread t of the fragment; 4 channels per step
+      constexpr int CD = D >= 128 ? 32 : 16;
+      const int c0 = blk * 16, chunk = c0 / CD, ft = chunk & 3, j0 = (chunk >> 2) * 8 + (c0 % CD) / 4;
+      const int fl = (row & 7) * 4 + ft, nt = row >> 3;
+      uint4* eo = qe + (nt * NS + j0) * 32 + fl;
+      uint4* fo = qf + (nt * NS + j0) * 32 + fl;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 v;
+        if constexpr (QBF) {
+          v = make_uint4(pack_bf16(a[4 * j], a[4 * j + 1]), pack_bf16(a[4 * j + 2], a[4 * j + 3]), 0u, 0u);
+        } else {
+          split_bf16(a[4 * j], a[4 * j + 1], v.x, v.z);
+          split_bf16(a[4 * j + 2], a[4 * j + 3], v.y, v.w);
+        }
+        eo[j * 32] = v;
+      }
+      if (p.k.rotate) fwht16(a);
+      const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;            // carried by the query, so that factors are >= 0
+      float mx = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(a[k]));
+#pragma unroll
+      for (int o = BPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+      int e = (int)(__float_as_uint(mx) >> 23) - 127;                  // floor(log2), exact for normal values
+      e = mx > 0.0f && mx <= FLT_MAX ? max(-100, min(100, e)) : 0;
+      const float down = sign * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 v;
+        split_f16(a[4 * j] * down, a[4 * j + 1] * down, v.x, v.z);
+        split_f16(a[4 * j + 2] * down, a[4 * j + 3] * down, v.y, v.w);
+        fo[j * 32] = v;
+      }
+      if (blk == 0) {
+        rowfac[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+        // positions this row sees: all before the limit (rows past R restrict nothing and are not written)
+        limit[row] = p.causal && r < p.R ? max(sq.len - p.Tq + r / p.G + 1, 0) : sq.len;
+      }
+    }
+    __syncthreads();
+
+    float O[NO][NT][4], m[NT][2], l[NT][2], fac[NT][2];
+    int lim[NT][2];                               // positions each column's row sees: all before this one
+    int lim_min = INT_MAX;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float s0 = kKaPShift - finite_or_zero(m[n][0]), s1 = kKaPShift - finite_or_zero(m[n][1]);
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float p0 = ex2(fmaf(S[a][n][2 * h], fac[n][0], s0)), p1 = ex2(fmaf(S[a][n][2 * h + 1], fac[n][1], s1));
-          if (!full) {                           // -Inf times a zero factor would be NaN
-            p0 = S[a][n][2 * h] == -INFINITY ? 0.0f : p0;
-            p1 = S[a][n][2 * h + 1] == -INFINITY ? 0.0f : p1;
-          }
-          l[n][0] += p0;
-          l[n][1] += p1;
-          pb[a][n][h] = movmatrix(pack_f16(p0, p1));
-        }
-    }
-    // ---- O^T += V^T P^T: rows are channels, the 16 k positions the tokens 4 r + t of the fragment order ----
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      uint32_t vw[4][VW], vs[2][VB];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * a + 4 * r + t;
-        if constexpr (VW == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kVC + ((row * Sh::kCodeRow + g * 16) ^ ((row & 3) << 5)));
-          vw[r][0] = v.x, vw[r][1] = v.y, vw[r][2] = v.z, vw[r][3] = v.w;
-        } else if constexpr (VW == 2) {
-          const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kVC + ((row * Sh::kCodeRow + g * 8) ^ ((row >> 1 & 1) << 5)));
-          vw[r][0] = v.x, vw[r][1] = v.y;
-        } else {
-          vw[r][0] = *reinterpret_cast<const uint32_t*>(st + Sh::kVC + row * Sh::kCodeRow + g * 4);
-        }
-      }
-#pragma unroll
-      for (int q2 = 0; q2 < 2; ++q2) {
-        const unsigned char* s0 = st + Sh::kVS + (16 * a + 8 * q2 + t) * Sh::kScaleRow;
-        const unsigned char* s1 = s0 + 4 * Sh::kScaleRow;
-        if constexpr (VB == 2) {
-          const uint32_t u0 = *reinterpret_cast<const unsigned short*>(s0 + 2 * g), u1 = *reinterpret_cast<const unsigned short*>(s1 + 2 * g);
-          vs[q2][0] = e4m3x2_f16x2(__byte_perm(u0, u1, 0x0040));
-          vs[q2][1] = e4m3x2_f16x2(__byte_perm(u0, u1, 0x0051));
-        } else {
-          const int blk = D == 128 ? g : g >> 1;
-          vs[q2][0] = e4m3x2_f16x2(s0[blk] | (uint32_t)s1[blk] << 8);
-        }
-      }
-      uint32_t nan_tok[VB];
-      if (!full) {
-        // a poisoned block (scale NaN) of a token that only some of the columns see: 0 * NaN would reach the
-        // others through the product, so its scale becomes 0 and the columns that do see it turn NaN below
-#pragma unroll
-        for (int vb = 0; vb < VB; ++vb) {
-          nan_tok[vb] = 0;
-#pragma unroll
-          for (int q2 = 0; q2 < 2; ++q2) {
-            const uint32_t u = vs[q2][vb];
-            if ((u & 0x7FFFu) > 0x7C00u) nan_tok[vb] |= 1u << (16 * a + 8 * q2 + t), vs[q2][vb] &= 0xFFFF0000u;
-            if ((u >> 16 & 0x7FFFu) > 0x7C00u) nan_tok[vb] |= 1u << (16 * a + 8 * q2 + 4 + t), vs[q2][vb] &= 0x0000FFFFu;
-          }
-          nan_tok[vb] |= __shfl_xor_sync(0xFFFFFFFFu, nan_tok[vb], 1);
-          nan_tok[vb] |= __shfl_xor_sync(0xFFFFFFFFu, nan_tok[vb], 2);
-        }
-      }
-#pragma unroll
-      for (int wd = 0; wd < VW; ++wd) {
-        constexpr uint32_t LO = 0x0F0F0F0Fu;
-        uint32_t hx[2][4], hy[2][4];             // even and odd channels, (token 4 r + t, token 4 (r + 1) + t)
-#pragma unroll
-        for (int q2 = 0; q2 < 2; ++q2) {
-          const uint32_t u = vw[2 * q2][wd], v = vw[2 * q2 + 1][wd];
-          e2m1x8((u & LO) | ((v << 4) & ~LO), hx[q2]);
-          e2m1x8(((u >> 4) & LO) | (v & ~LO), hy[q2]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            hx[q2][k] = hmul2(hx[q2][k], vs[q2][VB == 2 ? wd >> 1 : 0]);
-            hy[q2][k] = hmul2(hy[q2][k], vs[q2][VB == 2 ? wd >> 1 : 0]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816<false>(O[4 * wd + k][n], hx[0][k], hy[0][k], hx[1][k], hy[1][k], pb[a][n][0], pb[a][n][1]);
-      }
-      if (!full) {
-#pragma unroll
-        for (int vb = 0; vb < VB; ++vb)
-          if (nan_tok[vb]) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                if (nan_tok[vb] & seen_of(n, c, tok0, vm)) {
-#pragma unroll
-                  for (int k = 0; k < NO / VB; ++k) O[vb * (NO / VB) + k][n][c] = O[vb * (NO / VB) + k][n][c + 2] = NAN;
-                }
-              }
-          }
-      }
-    }
-  }
-
-  // ---- the middle's sums: undo the numerators' scale, apply g_v, turn back along the channels ----
-  if (n_my > 0) {
-    constexpr float kUndo = 1.0f / 1024.0f;
-    const float gv = p.v.gscale[p.v.gstride * sq.s] * kUndo;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        l[n][c] *= kUndo;
-        if (p.v.rotate) {
-          if constexpr (D == 64) {
-            // 8 channels here, the other 8 of the block in the lane of g ^ 1
-            float a[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[2 * i] = O[i][n][c], a[2 * i + 1] = O[i][n][c + 2];
-#pragma unroll
-            for (int h = 1; h < 8; h <<= 1)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if ((i & h) == 0) {
-                  const float u = a[i], v = a[i + h];
-                  a[i] = u + v;
-                  a[i + h] = u - v;
-                }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float o = __shfl_xor_sync(0xFFFFFFFFu, a[i], 4);
-              a[i] = 0.25f * (g & 1 ? o - a[i] : a[i] + o);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) O[i][n][c] = a[2 * i], O[i][n][c + 2] = a[2 * i + 1];
-          } else {
-#pragma unroll
-            for (int blk = 0; blk < NO / 8; ++blk) {
-              float a[16];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) a[2 * i] = O[8 * blk + i][n][c], a[2 * i + 1] = O[8 * blk + i][n][c + 2];
-              fwht16(a);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) O[8 * blk + i][n][c] = a[2 * i], O[8 * blk + i][n][c + 2] = a[2 * i + 1];
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < NO; ++i) {
-          O[i][n][c] *= gv;
-          O[i][n][c + 2] *= gv;
-        }
+        m[n][c] = -INFINITY;
+        l[n][c] = 0.0f;
+        lim[n][c] = limit[8 * n + 2 * t + c];
+        lim_min = min(lim_min, lim[n][c]);
+        fac[n][c] = rowfac[8 * n + 2 * t + c];
       }
-  }
+#pragma unroll
+      for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) O[i][n][c] = 0.0f;
+    }
+    lim_min = min(lim_min, __shfl_xor_sync(0xFFFFFFFFu, lim_min, 1));
+    lim_min = min(lim_min, __shfl_xor_sync(0xFFFFFFFFu, lim_min, 2));
+    const int perm = (g >> 1) + 4 * (g & 1);      // the token of fragment row g (row g + 8: + 8)
 
-  // ---- the BF16 ends, 16 tokens at a time, spread over the ranges and their warps ----
-  const int sink_tiles = (sq.ns + 15) / 16, end_tiles = sink_tiles + (sq.nw + 15) / 16;
-  for (int64_t e64 = ch + (int64_t)active * w; e64 < end_tiles; e64 += (int64_t)active * kKaWarps) {
-    const int e = (int)e64;
-    const bool in_sink = e < sink_tiles;
-    const int r0 = 16 * (in_sink ? e : e - sink_tiles), cnt = min(16, (in_sink ? sq.ns : sq.nw) - r0);
-    const int64_t pos0 = in_sink ? r0 : (int64_t)sq.ns + sq.nm + r0;
-    const int rows = in_sink ? p.sink_rows : p.window_rows;
-    const int64_t mat = ((int64_t)sq.s * p.Hkv + kvh) * rows;
-    const bool cut = pos0 + cnt > lim_min;       // some row does not see all of the tile
-    auto row_at = [&](const KvSide& s, int r) -> const char* {
-      int at = r0 + r;
-      if (!in_sink) {
-        at += sq.head;
-        if (at >= rows) at -= rows;
-      }
-      return (in_sink ? s.sink : s.window) + (mat + at) * (D * 2);
+    // the tile's tokens (bit k: token k) that a column's row sees
+    auto seen_of = [&](int n, int c, int tok0, uint32_t vm) -> uint32_t {
+      const int rel = max(min(lim[n][c] - sq.ns - tok0, kKaTile), 0);
+      return vm & (rel >= 32 ? 0xFFFFFFFFu : (1u << rel) - 1u);
     };
-    float S[NT][4];
+
+    // The reference m of a row's numerators follows its maximum lazily: while no score of the tile passes it by more
+    // than kKaSlack, m and everything summed under it stay (one vote); else m becomes the tile's maximum and the
+    // sums are rescaled.
+    auto raise = [&](float (&mx)[NT][2]) {
+      bool up = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) up |= mx[n][0] > m[n][0] + kKaSlack || mx[n][1] > m[n][1] + kKaSlack;
+      if (!__any_sync(0xFFFFFFFFu, up)) return;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) S[n][c] = 0.0f;
-    const bool ok0 = perm < cnt, ok1 = perm + 8 < cnt;
-    const char* k0 = row_at(p.k, ok0 ? perm : 0);
-    const char* k1 = row_at(p.k, ok1 ? perm + 8 : 0);
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int cc = 0; cc < KCH; ++cc)
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int v8 = 0; v8 < KW; ++v8) {          // 8 channels of the chunk: two steps
-        uint4 u = make_uint4(0, 0, 0, 0), v = u;
-        const int at = ((t + 4 * cc) * (KW * 8) + v8 * 8) * 2;
-        if (ok0) u = *reinterpret_cast<const uint4*>(k0 + at);
-        if (ok1) v = *reinterpret_cast<const uint4*>(k1 + at);
-        const int j = cc * 8 + v8 * 2;
+          for (int o = 4; o < 32; o <<= 1) mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xFFFFFFFFu, mx[n][c], o));
+          const float mn = fmaxf(m[n][c], mx[n][c]);
+          const float al = ex2(m[n][c] - finite_or_zero(mn));
+          m[n][c] = mn;
+          l[n][c] *= al;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 qa = qe[(n * NS + j) * 32 + lane], qb = qe[(n * NS + j + 1) * 32 + lane];
-          mma16816<true>(S[n], u.x, v.x, u.y, v.y, qa.x, qa.y);
-          mma16816<true>(S[n], u.z, v.z, u.w, v.w, qb.x, qb.y);
-          if constexpr (!QBF) {                  // a BF16 query is its first term
-            mma16816<true>(S[n], u.x, v.x, u.y, v.y, qa.z, qa.w);
-            mma16816<true>(S[n], u.z, v.z, u.w, v.w, qb.z, qb.w);
+          for (int i = 0; i < NO; ++i) {
+            O[i][n][c] *= al;
+            O[i][n][c + 2] *= al;
           }
         }
+    };
+
+    if (n_my > 0) {
+      const float gk = p.k.gscale[p.k.gstride * sq.s] * fabsf(p.scale_log2);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        fac[n][0] *= gk;
+        fac[n][1] *= gk;
       }
-    float mx[NT][2];
+    }
+    // One tile of 32 tokens.  FULL: all of them exist and every row sees them.
+    auto work = [&](auto full, const unsigned char* st, int tok0, uint32_t vm) {
+      constexpr bool FULL = decltype(full)::value;
+      // ---- S^T = K Q^T: rows are tokens (two tiles of 16), columns query rows ----
+      float S[2][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        mx[n][c] = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = perm + 8 * h;
-          float& s = S[n][c + 2 * h];
-          s = r < cnt && pos0 + r < lim[n][c] ? s * p.scale_log2 : -INFINITY;
-          mx[n][c] = fmaxf(mx[n][c], s);
-        }
-      }
-    raise(mx);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float ms = finite_or_zero(m[n][c]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          S[n][c + 2 * h] = ex2(S[n][c + 2 * h] - ms);
-          l[n][c] += S[n][c + 2 * h];
-        }
-      }
-    uint32_t ph[NT][2], pl[NT][2];               // numerators as two BF16 terms
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t a, c;
-        split_bf16(S[n][2 * h], S[n][2 * h + 1], a, c);
-        ph[n][h] = movmatrix(a);
-        pl[n][h] = movmatrix(c);
-      }
-#pragma unroll
-    for (int v8 = 0; v8 < D / 64; ++v8) {        // 8 channels of the thread's chunk
-      uint4 vv[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool ok = 4 * r + t < cnt;
-        vv[r] = make_uint4(0, 0, 0, 0);
-        if (ok) vv[r] = *reinterpret_cast<const uint4*>(row_at(p.v, 4 * r + t) + (g * (D / 8) + v8 * 8) * 2);
-      }
-      if (!cut) {
+      for (int cc = 0; cc < KCH; ++cc) {
+        uint32_t kw[4][KW], ks[4][KW / 2];         // rows perm + 8 k of the tile; scales doubled into both halves
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t w0 = (&vv[0].x)[k], w1 = (&vv[1].x)[k], w2 = (&vv[2].x)[k], w3 = (&vv[3].x)[k];
-          const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-          const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-            mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+          const int row = perm + 8 * k;
+          const uint32_t sw = ((uint32_t)row >> 2 & 1u) << 6;
+          if constexpr (KW == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kKC + ((row * Sh::kCodeRow + (t + 4 * cc) * 16) ^ sw));
+            kw[k][0] = v.x, kw[k][1] = v.y, kw[k][2] = v.z, kw[k][3] = v.w;
+            const uint32_t h = e4m3x2_f16x2(*reinterpret_cast<const unsigned short*>(st + Sh::kKS + row * Sh::kScaleRow + 2 * t + 8 * cc));
+            ks[k][0] = both_lo(h);
+            ks[k][1] = both_hi(h);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kKC + ((row * Sh::kCodeRow + t * 8) ^ sw));
+            kw[k][0] = v.x, kw[k][1] = v.y;
+            ks[k][0] = both_lo(e4m3x2_f16x2(st[Sh::kKS + row * Sh::kScaleRow + t]));
           }
         }
-      } else {
-        // tokens that some rows do not see: added token by token, so that infinities and NaN of a hidden
-        // token reach no row (a product would multiply them by its zero numerator)
+#pragma unroll
+        for (int wd = 0; wd < KW; ++wd) {          // a word of 8 codes feeds two steps
+          uint32_t h[4][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            e2m1x8(kw[k][wd], h[k]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) h[k][c] = hmul2(h[k][c], ks[k][wd >> 1]);
+          }
+#pragma unroll
+          for (int j2 = 0; j2 < 2; ++j2) {
+            const int j = cc * 8 + wd * 2 + j2;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint4 qv = qf[(n * NS + j) * 32 + lane];
+#pragma unroll
+              for (int a = 0; a < 2; ++a) {
+                if (j == 0) mma16816_zero(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
+                else mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
+                mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.z, qv.w);
+              }
+            }
+          }
+        }
+      }
+      // ---- numerators (fac >= 0: maxima are taken before it is applied) ----
+      float mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if constexpr (!FULL) {
+            const uint32_t seen = seen_of(n, c, tok0, vm);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!(seen >> (16 * a + 8 * h + perm) & 1u)) S[a][n][c + 2 * h] = -INFINITY;
+          }
+          mx[n][c] = fac[n][c] * fmaxf(fmaxf(S[0][n][c], S[0][n][c + 2]), fmaxf(S[1][n][c], S[1][n][c + 2]));
+        }
+      raise(mx);
+      uint32_t pb[2][NT][2];                       // the second product's B fragments (tokens x query rows)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float s0 = kKaPShift - finite_or_zero(m[n][0]), s1 = kKaPShift - finite_or_zero(m[n][1]);
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float p0 = ex2(fmaf(S[a][n][2 * h], fac[n][0], s0)), p1 = ex2(fmaf(S[a][n][2 * h + 1], fac[n][1], s1));
+            if constexpr (!FULL) {                           // -Inf times a zero factor would be NaN
+              p0 = S[a][n][2 * h] == -INFINITY ? 0.0f : p0;
+              p1 = S[a][n][2 * h + 1] == -INFINITY ? 0.0f : p1;
+            }
+            l[n][0] += p0;
+            l[n][1] += p1;
+            pb[a][n][h] = movmatrix(pack_f16(p0, p1));
+          }
+      }
+      // ---- O^T += V^T P^T: rows are channels, the 16 k positions the tokens 4 r + t of the fragment order ----
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        uint32_t vw[4][VW], vs[2][VB];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          for (int tt = 0; tt < 4; ++tt) {
-            uint32_t wd[4];
+          const int row = 16 * a + 4 * r + t;
+          if constexpr (VW == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kVC + ((row * Sh::kCodeRow + g * 16) ^ ((row & 3) << 5)));
+            vw[r][0] = v.x, vw[r][1] = v.y, vw[r][2] = v.z, vw[r][3] = v.w;
+          } else if constexpr (VW == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kVC + ((row * Sh::kCodeRow + g * 8) ^ ((row >> 1 & 1) << 5)));
+            vw[r][0] = v.x, vw[r][1] = v.y;
+          } else {
+            vw[r][0] = *reinterpret_cast<const uint32_t*>(st + Sh::kVC + row * Sh::kCodeRow + g * 4);
+          }
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) wd[k] = __shfl_sync(0xFFFFFFFFu, (&vv[r].x)[k], g * 4 + tt);
-            const int tk = 4 * r + tt, fr = 2 * tt + (r & 1);     // the token's fragment row is fr + 8 (r >> 1)
+        for (int q2 = 0; q2 < 2; ++q2) {
+          const unsigned char* s0 = st + Sh::kVS + (16 * a + 8 * q2 + t) * Sh::kScaleRow;
+          const unsigned char* s1 = s0 + 4 * Sh::kScaleRow;
+          if constexpr (VB == 2) {
+            const uint32_t u0 = *reinterpret_cast<const unsigned short*>(s0 + 2 * g), u1 = *reinterpret_cast<const unsigned short*>(s1 + 2 * g);
+            vs[q2][0] = e4m3x2_f16x2(__byte_perm(u0, u1, 0x0040));
+            vs[q2][1] = e4m3x2_f16x2(__byte_perm(u0, u1, 0x0051));
+          } else {
+            const int blk = D == 128 ? g : g >> 1;
+            vs[q2][0] = e4m3x2_f16x2(s0[blk] | (uint32_t)s1[blk] << 8);
+          }
+        }
+        uint32_t nan_tok[VB];
+        if constexpr (!FULL) {
+          // a poisoned block (scale NaN) of a token that only some of the columns see: 0 * NaN would reach the
+          // others through the product, so its scale becomes 0 and the columns that do see it turn NaN below
+#pragma unroll
+          for (int vb = 0; vb < VB; ++vb) {
+            nan_tok[vb] = 0;
+#pragma unroll
+            for (int q2 = 0; q2 < 2; ++q2) {
+              const uint32_t u = vs[q2][vb];
+              if ((u & 0x7FFFu) > 0x7C00u) nan_tok[vb] |= 1u << (16 * a + 8 * q2 + t), vs[q2][vb] &= 0xFFFF0000u;
+              if ((u >> 16 & 0x7FFFu) > 0x7C00u) nan_tok[vb] |= 1u << (16 * a + 8 * q2 + 4 + t), vs[q2][vb] &= 0x0000FFFFu;
+            }
+            nan_tok[vb] |= __shfl_xor_sync(0xFFFFFFFFu, nan_tok[vb], 1);
+            nan_tok[vb] |= __shfl_xor_sync(0xFFFFFFFFu, nan_tok[vb], 2);
+          }
+        }
+#pragma unroll
+        for (int wd = 0; wd < VW; ++wd) {
+          constexpr uint32_t LO = 0x0F0F0F0Fu;
+          uint32_t hx[2][4], hy[2][4];             // even and odd channels, (token 4 r + t, token 4 (r + 1) + t)
+#pragma unroll
+          for (int q2 = 0; q2 < 2; ++q2) {
+            const uint32_t u = vw[2 * q2][wd], v = vw[2 * q2 + 1][wd];
+            e2m1x8(pick(u, v << 4, LO), hx[q2]);
+            e2m1x8(pick(u >> 4, v, LO), hy[q2]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              hx[q2][k] = hmul2(hx[q2][k], vs[q2][VB == 2 ? wd >> 1 : 0]);
+              hy[q2][k] = hmul2(hy[q2][k], vs[q2][VB == 2 ? wd >> 1 : 0]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
+              mma16816<false>(O[4 * wd + k][n], hx[0][k], hy[0][k], hx[1][k], hy[1][k], pb[a][n][0], pb[a][n][1]);
+        }
+        if constexpr (!FULL) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const float pr = __shfl_sync(0xFFFFFFFFu, S[n][c + 2 * (r >> 1)], fr * 4 + t);
-                if (tk < cnt && pos0 + tk < lim[n][c]) {
+          for (int vb = 0; vb < VB; ++vb)
+            if (nan_tok[vb]) {
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    O[4 * v8 + k][n][c] = fmaf(pr, bf16lo(wd[k]), O[4 * v8 + k][n][c]);
-                    O[4 * v8 + k][n][c + 2] = fmaf(pr, bf16hi(wd[k]), O[4 * v8 + k][n][c + 2]);
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  if (nan_tok[vb] & seen_of(n, c, tok0, vm)) {
+#pragma unroll
+                    for (int k = 0; k < NO / VB; ++k) O[vb * (NO / VB) + k][n][c] = O[vb * (NO / VB) + k][n][c + 2] = NAN;
                   }
                 }
+            }
+        }
+      }
+    };
+    const int mid_seen = lim_min - sq.ns;         // every row sees the middle's tokens before this one
+    int stage = 0, ahead = ST - 1;                // stages of tile i and of the tile issued with it
+    for (int i = 0; i < n_my; ++i) {
+      cp_async_wait<ST - 2>();
+      __syncwarp();
+      {
+        const int a = next[0], c = next[1], k = i + ST - 1;
+        look_up(k + 1);
+        if (k < n_my) issue(k, ahead, a, c);
+        cp_async_commit();
+      }
+      const unsigned char* st = ring + stage * Sh::kStageBytes;
+      const int tok0 = (t_first + i * kKaWarps) * kKaTile;
+      if (!(partial >> (i & 31) & 1u) && tok0 + kKaTile <= mid_seen) {
+        work(std::true_type{}, st, tok0, 0xFFFFFFFFu);
+      } else {
+        const uint32_t vm = partial >> (i & 31) & 1u ? vms[w * ST + stage] : 0xFFFFFFFFu;
+        partial &= ~(1u << (i & 31));
+        work(std::false_type{}, st, tok0, vm);
+      }
+      stage = stage == ST - 1 ? 0 : stage + 1;
+      ahead = ahead == ST - 1 ? 0 : ahead + 1;
+    }
+
+    // ---- the middle's sums: undo the numerators' scale, apply g_v, turn back along the channels ----
+    if (n_my > 0) {
+      constexpr float kUndo = 1.0f / 1024.0f;
+      const float gv = p.v.gscale[p.v.gstride * sq.s] * kUndo;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          l[n][c] *= kUndo;
+          if (p.v.rotate) {
+            if constexpr (D == 64) {
+              // 8 channels here, the other 8 of the block in the lane of g ^ 1
+              float a[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) a[2 * i] = O[i][n][c], a[2 * i + 1] = O[i][n][c + 2];
+#pragma unroll
+              for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if ((i & h) == 0) {
+                    const float u = a[i], v = a[i + h];
+                    a[i] = u + v;
+                    a[i + h] = u - v;
+                  }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float o = __shfl_xor_sync(0xFFFFFFFFu, a[i], 4);
+                a[i] = 0.25f * (g & 1 ? o - a[i] : a[i] + o);
               }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) O[i][n][c] = a[2 * i], O[i][n][c + 2] = a[2 * i + 1];
+            } else {
+#pragma unroll
+              for (int blk = 0; blk < NO / 8; ++blk) {
+                float a[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[2 * i] = O[8 * blk + i][n][c], a[2 * i + 1] = O[8 * blk + i][n][c + 2];
+                fwht16(a);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) O[8 * blk + i][n][c] = a[2 * i], O[8 * blk + i][n][c + 2] = a[2 * i + 1];
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < NO; ++i) {
+            O[i][n][c] *= gv;
+            O[i][n][c + 2] *= gv;
+          }
+        }
+    }
+
+    // ---- the BF16 ends, 16 tokens a tile ----
+    for (int e = e_first; e < e_end; e += kKaWarps) {
+      const bool in_sink = e < sink_tiles;
+      const int r0 = 16 * (in_sink ? e : e - sink_tiles), cnt = min(16, (in_sink ? sq.ns : sq.nw) - r0);
+      const int pos0 = in_sink ? r0 : sq.ns + sq.nm + r0;
+      const int rows = in_sink ? p.sink_rows : p.window_rows;
+      const int64_t mat = ((int64_t)sq.s * p.Hkv + kvh) * rows;
+      const bool cut = pos0 + cnt > lim_min;       // some row does not see all of the tile
+      auto row_at = [&](const KvSide& s, int r) -> const char* {
+        int at = r0 + r;
+        if (!in_sink) {
+          at += sq.head;
+          if (at >= rows) at -= rows;
+        }
+        return (in_sink ? s.sink : s.window) + (mat + at) * (D * 2);
+      };
+      float S[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[n][c] = 0.0f;
+      const bool ok0 = perm < cnt, ok1 = perm + 8 < cnt;
+      const char* k0 = row_at(p.k, ok0 ? perm : 0);
+      const char* k1 = row_at(p.k, ok1 ? perm + 8 : 0);
+#pragma unroll
+      for (int cc = 0; cc < KCH; ++cc)
+#pragma unroll
+        for (int v8 = 0; v8 < KW; ++v8) {          // 8 channels of the chunk: two steps
+          uint4 u = make_uint4(0, 0, 0, 0), v = u;
+          const int at = ((t + 4 * cc) * (KW * 8) + v8 * 8) * 2;
+          if (ok0) u = *reinterpret_cast<const uint4*>(k0 + at);
+          if (ok1) v = *reinterpret_cast<const uint4*>(k1 + at);
+          const int j = cc * 8 + v8 * 2;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 qa = qe[(n * NS + j) * 32 + lane], qb = qe[(n * NS + j + 1) * 32 + lane];
+            mma16816<true>(S[n], u.x, v.x, u.y, v.y, qa.x, qa.y);
+            mma16816<true>(S[n], u.z, v.z, u.w, v.w, qb.x, qb.y);
+            if constexpr (!QBF) {                  // a BF16 query is its first term
+              mma16816<true>(S[n], u.x, v.x, u.y, v.y, qa.z, qa.w);
+              mma16816<true>(S[n], u.z, v.z, u.w, v.w, qb.z, qb.w);
+            }
+          }
+        }
+      float mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mx[n][c] = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = perm + 8 * h;
+            float& s = S[n][c + 2 * h];
+            s = r < cnt && pos0 + r < lim[n][c] ? s * p.scale_log2 : -INFINITY;
+            mx[n][c] = fmaxf(mx[n][c], s);
+          }
+        }
+      raise(mx);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float ms = finite_or_zero(m[n][c]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            S[n][c + 2 * h] = ex2(S[n][c + 2 * h] - ms);
+            l[n][c] += S[n][c + 2 * h];
+          }
+        }
+      uint32_t ph[NT][2], pl[NT][2];               // numerators as two BF16 terms
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a, c;
+          split_bf16(S[n][2 * h], S[n][2 * h + 1], a, c);
+          ph[n][h] = movmatrix(a);
+          pl[n][h] = movmatrix(c);
+        }
+#pragma unroll
+      for (int v8 = 0; v8 < D / 64; ++v8) {        // 8 channels of the thread's chunk
+        uint4 vv[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool ok = 4 * r + t < cnt;
+          vv[r] = make_uint4(0, 0, 0, 0);
+          if (ok) vv[r] = *reinterpret_cast<const uint4*>(row_at(p.v, 4 * r + t) + (g * (D / 8) + v8 * 8) * 2);
+        }
+        if (!cut) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w0 = (&vv[0].x)[k], w1 = (&vv[1].x)[k], w2 = (&vv[2].x)[k], w3 = (&vv[3].x)[k];
+            const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+            const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+              mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+            }
+          }
+        } else {
+          // tokens that some rows do not see: added token by token, so that infinities and NaN of a hidden
+          // token reach no row (a product would multiply them by its zero numerator)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            for (int tt = 0; tt < 4; ++tt) {
+              uint32_t wd[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) wd[k] = __shfl_sync(0xFFFFFFFFu, (&vv[r].x)[k], g * 4 + tt);
+              const int tk = 4 * r + tt, fr = 2 * tt + (r & 1);     // the token's fragment row is fr + 8 (r >> 1)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const float pr = __shfl_sync(0xFFFFFFFFu, S[n][c + 2 * (r >> 1)], fr * 4 + t);
+                  if (tk < cnt && pos0 + tk < lim[n][c]) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      O[4 * v8 + k][n][c] = fmaf(pr, bf16lo(wd[k]), O[4 * v8 + k][n][c]);
+                      O[4 * v8 + k][n][c + 2] = fmaf(pr, bf16hi(wd[k]), O[4 * v8 + k][n][c + 2]);
+                    }
+                  }
+                }
+            }
           }
         }
       }
     }
-  }
 
-  // ---- join the warps ----
+    // ---- join the warps ----
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], o);
-      if (g == 0) stat[w * ROWS + 8 * n + 2 * t + c] = make_float2(m[n][c], l[n][c]);
-    }
-  cp_async_wait<0>();
-  __syncthreads();                               // every warp is done with its ring: the accumulators take its place
-  float* acc = reinterpret_cast<float*>(smem);
+        for (int o = 4; o < 32; o <<= 1) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], o);
+        if (g == 0) stat[w * ROWS + 8 * n + 2 * t + c] = make_float2(m[n][c], l[n][c]);
+      }
+    cp_async_wait<0>();
+    __syncthreads();                               // every warp is done with its ring: the accumulators take its place
+    float* acc = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int row = 8 * n + 2 * t + c;
-      float mm = -INFINITY;
+      for (int c = 0; c < 2; ++c) {
+        const int row = 8 * n + 2 * t + c;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kKaWarps; ++k) mm = fmaxf(mm, stat[k * ROWS + row].x);
+        const float f = ex2(m[n][c] - finite_or_zero(mm));
+        float* a = acc + (w * ROWS + row) * Sm::kAccRow + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < NO; ++i) *reinterpret_cast<float2*>(a + 2 * i) = make_float2(O[i][n][c] * f, O[i][n][c + 2] * f);
+      }
+    __syncthreads();
+    for (int v = tid; v < ROWS * (D / 4); v += kKaWarps * 32) {
+      const int row = v / (D / 4), d = 4 * (v % (D / 4)), r = row_tile * ROWS + row;
+      if (r >= p.R) continue;
+      float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
       for (int k = 0; k < kKaWarps; ++k) mm = fmaxf(mm, stat[k * ROWS + row].x);
-      const float f = ex2(m[n][c] - finite_or_zero(mm));
-      float* a = acc + (w * ROWS + row) * Sm::kAccRow + g * (D / 8);
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < NO; ++i) *reinterpret_cast<float2*>(a + 2 * i) = make_float2(O[i][n][c] * f, O[i][n][c + 2] * f);
+      for (int k = 0; k < kKaWarps; ++k) {
+        const float2 ml = stat[k * ROWS + row];
+        ll = fmaf(ml.y, ex2(ml.x - finite_or_zero(mm)), ll);
+        const float4 x = *reinterpret_cast<const float4*>(acc + (k * ROWS + row) * Sm::kAccRow + d);
+        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+      }
+      const int i = r / p.G, hq = kvh * p.G + r % p.G;
+      if (first_unit > 0 || last_unit < units) {     // shared with other parts
+        const int64_t at = ((int64_t)part * 2 + (first_unit > 0 ? 0 : 1)) * ROWS + row;
+        *reinterpret_cast<float4*>(p.ws_o + at * D + d) = s;
+        if (d == 0) p.ws_ml[at] = make_float2(mm, ll);
+      } else {
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;   // no visible token: zeros
+        const int64_t at = b * p.o_sb + hq * p.o_sh + i * p.o_st + d;
+        ka_store<QBF>(p.out, at, s.x * inv);
+        ka_store<QBF>(p.out, at + 1, s.y * inv);
+        ka_store<QBF>(p.out, at + 2, s.z * inv);
+        ka_store<QBF>(p.out, at + 3, s.w * inv);
+        if (d == 0 && p.lse) p.lse[((int64_t)b * p.Hq + hq) * p.Tq + i] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+      }
     }
-  __syncthreads();
-  for (int u = tid; u < ROWS * (D / 4); u += kKaWarps * 32) {
-    const int row = u / (D / 4), d = 4 * (u % (D / 4)), r = row_tile * ROWS + row;
-    if (r >= p.R) continue;
-    float mm = -INFINITY, ll = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kKaWarps; ++k) mm = fmaxf(mm, stat[k * ROWS + row].x);
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < kKaWarps; ++k) {
-      const float2 ml = stat[k * ROWS + row];
-      ll = fmaf(ml.y, ex2(ml.x - finite_or_zero(mm)), ll);
-      const float4 v = *reinterpret_cast<const float4*>(acc + (k * ROWS + row) * Sm::kAccRow + d);
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
-    const int i = r / p.G, hq = kvh * p.G + r % p.G;
-    if (active > 1) {
-      const int64_t at = ((int64_t)(b * p.Hkv + kvh) * p.R + r) * p.nch + ch;
-      *reinterpret_cast<float4*>(p.ws_o + at * D + d) = s;
-      if (d == 0) p.ws_ml[at] = make_float2(mm, ll);
-    } else {
-      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;   // no visible token: zeros
-      const int64_t at = b * p.o_sb + hq * p.o_sh + i * p.o_st + d;
-      ka_store<QBF>(p.out, at, s.x * inv);
-      ka_store<QBF>(p.out, at + 1, s.y * inv);
-      ka_store<QBF>(p.out, at + 2, s.z * inv);
-      ka_store<QBF>(p.out, at + 3, s.w * inv);
-      if (d == 0 && p.lse) p.lse[((int64_t)b * p.Hq + hq) * p.Tq + i] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
-    }
+    __syncthreads();                             // the next job takes the shared memory
   }
 }
 
-// Joins the ranges of the sequences that have more than one: a CTA per query row, warps striding the ranges.
-template <int D, bool QBF>
-__global__ void __launch_bounds__(128) kv_attn_combine_kernel(const __grid_constant__ KvAttnParams p) {
-  constexpr int E = D / 32;                      // channels per lane
-  __shared__ float part[4][D];
-  __shared__ float lpart[4];
+// Joins the jobs that cuts fall into: the CTAs of the first cut of each, one per query row.
+template <int D, int NT, bool QBF>
+__global__ void __launch_bounds__(kKaJoinWarps * 32) kv_attn_combine_kernel(const __grid_constant__ KvAttnParams p) {
+  constexpr int E = D / 32, ROWS = 8 * NT;       // channels per lane
+  __shared__ float part[kKaJoinWarps][D];
+  __shared__ float lpart[kKaJoinWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int row = blockIdx.x, r = row % p.R, bk = row / p.R, kvh = bk % p.Hkv, b = bk / p.Hkv;
-  const KaSeq sq = ka_sequence(p, b);
-  int per, active;
-  ka_ranges(sq.nm, p.nch, per, active);
-  if (active == 1) return;
-  const float2* ml = p.ws_ml + (int64_t)row * p.nch;
-  const float* o = p.ws_o + (int64_t)row * p.nch * D + lane * E;
+  const int4 job = p.ws_meta[blockIdx.x];        // sequence, head and row tile, parts that share it
+  if (job.w == 0) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, row = blockIdx.y;
+  const int kvh = job.y / p.row_tiles, r = (job.y - kvh * p.row_tiles) * ROWS + row, b = job.x;
+  if (r >= p.R) return;
+  // piece 0: the end of the part before the cut; piece i: the beginning of part blockIdx.x - 1 + i
+  auto piece = [&](int i) -> int64_t { return ((int64_t)(blockIdx.x - 1 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
   float mm = -INFINITY;
-  for (int c = lane; c < active; c += 32) mm = fmaxf(mm, ml[c].x);
+  for (int i = lane; i < job.z; i += 32) mm = fmaxf(mm, p.ws_ml[piece(i)].x);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, k));
   const float ms = finite_or_zero(mm);
@@ -942,13 +1057,14 @@ __global__ void __launch_bounds__(128) kv_attn_combine_kernel(const __grid_const
 #pragma unroll
   for (int k = 0; k < E; ++k) s[k] = 0.0f;
 #pragma unroll 4
-  for (int c = w; c < active; c += 4) {
-    const float2 st = ml[c];
+  for (int i = w; i < job.z; i += kKaJoinWarps) {
+    const int64_t at = piece(i);
+    const float2 st = p.ws_ml[at];
     const float f = ex2(st.x - ms);
     ll = fmaf(st.y, f, ll);
     float v[E];
 #pragma unroll
-    for (int k = 0; k < E; k += 2) *reinterpret_cast<float2*>(v + k) = *reinterpret_cast<const float2*>(o + (int64_t)c * D + k);
+    for (int k = 0; k < E; k += 2) *reinterpret_cast<float2*>(v + k) = *reinterpret_cast<const float2*>(p.ws_o + at * D + lane * E + k);
 #pragma unroll
     for (int k = 0; k < E; ++k) s[k] = fmaf(v[k], f, s[k]);
   }
@@ -956,12 +1072,18 @@ __global__ void __launch_bounds__(128) kv_attn_combine_kernel(const __grid_const
   for (int k = 0; k < E; ++k) part[w][lane * E + k] = s[k];
   if (lane == 0) lpart[w] = ll;
   __syncthreads();
-  ll = (lpart[0] + lpart[1]) + (lpart[2] + lpart[3]);
+  ll = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kKaJoinWarps; ++k) ll += lpart[k];
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
   const int i = r / p.G, hq = kvh * p.G + r % p.G;
   const int64_t at = b * p.o_sb + hq * p.o_sh + i * p.o_st;
-  for (int d = threadIdx.x; d < D; d += 128)
-    ka_store<QBF>(p.out, at + d, ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) * inv);
+  for (int d = threadIdx.x; d < D; d += kKaJoinWarps * 32) {
+    float x = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kKaJoinWarps; ++k) x += part[k][d];
+    ka_store<QBF>(p.out, at + d, x * inv);
+  }
   if (threadIdx.x == 0 && p.lse)
     p.lse[((int64_t)b * p.Hq + hq) * p.Tq + i] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
 }
