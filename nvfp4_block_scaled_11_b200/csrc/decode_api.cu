@@ -36,7 +36,7 @@ int raise_smem(int bytes) {
 
 template <int D, int NT, bool QBF>
 int launch_kv_attention(const KvAttnParams& p, unsigned parts, bool join, cudaStream_t s) {
-  constexpr int smem = KaSmem<D, NT>::kBytes;
+  constexpr int smem = KaSmem<D, NT, QBF>::kBytes;
   if (int rc = raise_smem<kv_attn_kernel<D, NT, QBF>>(smem)) return rc;
   kv_attn_kernel<D, NT, QBF><<<parts, kKaWarps * 32, smem, s>>>(p);
   if (int rc = last_error()) return rc;
@@ -70,7 +70,7 @@ int launch_kv_attention_d(const KvAttnParams& p, bool bf, int nt, unsigned parts
 int ka_row_units(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 // CTAs of the attention kernel that an SM holds (its launch bounds and shared memory).
-int ka_ctas_per_sm(int64_t D, int nt) { return D == 256 ? 2 : D == 128 ? (nt == 1 ? 4 : 3) : (nt == 1 ? 5 : 4); }
+int ka_ctas_per_sm(int64_t D, int nt) { return D == 256 ? 2 : D == 128 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 4 : 3); }
 
 // One side of the cache: pointers and layout into the kernel's form.
 int ka_side(const nvfp4_kv_store& c, const nvfp4_kv_attention_desc& d, int64_t mid_rows, KvSide& o) {

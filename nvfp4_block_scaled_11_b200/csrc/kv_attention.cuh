@@ -86,14 +86,15 @@ struct KaShape {
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kRing = kKaWarps * kStages * kStageBytes;
 };
-template <int D, int NT>
+template <int D, int NT, bool QBF>
 struct KaSmem {
   static constexpr int kAccRow = D + 4;                                   // floats, padded
   static constexpr int kAcc = kKaWarps * 8 * NT * kAccRow * 4;            // the join of the warps reuses the ring
   static constexpr int kRing = KaShape<D>::kRing > kAcc ? KaShape<D>::kRing : kAcc;
-  static constexpr int kQ = NT * (D / 16) * 32 * 16;                      // one query operand (hi and lo)
+  static constexpr int kQ = NT * (D / 16) * 32 * 16;                      // the rotated query's fragments (hi and lo)
+  static constexpr int kQE = QBF ? kQ / 2 : kQ;                           // the query as given (a BF16 one is its first term)
   static constexpr int kStat = kKaWarps * 8 * NT * 8;
-  static constexpr int kBytes = kRing + 2 * kQ + kStat + 8 * NT * 8 + kKaWarps * KaShape<D>::kStages * 4;
+  static constexpr int kBytes = kRing + kQ + kQE + kStat + 8 * NT * 8 + kKaWarps * KaShape<D>::kStages * 4;
 };
 
 // ---- small instruction wrappers ----
@@ -111,6 +112,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -259,10 +263,10 @@ __device__ __forceinline__ void ka_store(char* out, int64_t i, float x) {
 
 // D: head_dim; NT: query rows / 8 of a CTA; QBF: q and out are BF16 (else FP16).
 template <int D, int NT, bool QBF>
-__global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 5 : 4))
+__global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3))
     kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
   using Sh = KaShape<D>;
-  using Sm = KaSmem<D, NT>;
+  using Sm = KaSmem<D, NT, QBF>;
   constexpr int ST = Sh::kStages, NS = D / 16 /* k16 steps */, NO = D / 16 /* m16 tiles of channels */;
   constexpr int KW = D >= 128 ? 4 : 2, KCH = D == 256 ? 2 : 1;      // code words per key chunk, chunks per thread
   constexpr int VW = D / 64;                                         // code words of V per thread and token
@@ -270,9 +274,10 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(128) unsigned char smem[];
   uint4* qf = reinterpret_cast<uint4*>(smem + Sm::kRing);            // rotated query, FP16 hi / lo, fragment order
-  uint4* qe = reinterpret_cast<uint4*>(smem + Sm::kRing + Sm::kQ);   // query as given, BF16 hi / lo
-  float2* stat = reinterpret_cast<float2*>(smem + Sm::kRing + 2 * Sm::kQ);
-  float* rowfac = reinterpret_cast<float*>(smem + Sm::kRing + 2 * Sm::kQ + Sm::kStat);
+  uint2* qe = reinterpret_cast<uint2*>(smem + Sm::kRing + Sm::kQ);   // query as given, BF16: first terms,
+  uint2* qr = qe + NT * NS * 32;                                     // and (FP16 only) second terms
+  float2* stat = reinterpret_cast<float2*>(smem + Sm::kRing + Sm::kQ + Sm::kQE);
+  float* rowfac = reinterpret_cast<float*>(smem + Sm::kRing + Sm::kQ + Sm::kQE + Sm::kStat);
   int* limit = reinterpret_cast<int*>(rowfac + ROWS);
   uint32_t* vms = reinterpret_cast<uint32_t*>(limit + ROWS);         // [warp][stage]: the tile's tokens that exist
   __shared__ int64_t scan[kKaWarps + 1];
@@ -373,9 +378,9 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
     const uint8_t* vc = p.v.codes + lane * 16;
     constexpr int RPP = 16 / Sh::kScaleRow, NP = kKaTile / RPP;        // scale rows per 16 bytes, pieces per tile and side
     const uint8_t* sc = (NP == 32 || lane < NP ? p.k.scales : p.v.scales) + lane % (NP / 2) * 16;   // NP < 32: keys', then values'
-    const bool pieces16 = p.k.vec16 && p.v.vec16;
-    const uint32_t head_rows = (uint32_t)p.Hkv * (uint32_t)p.page_rows, my_rows = (uint32_t)kvh * (uint32_t)p.page_rows;
     const int32_t* my_table = p.table ? p.table + (int64_t)sq.s * p.cols : nullptr;
+    const bool pieces16 = p.k.vec16 && p.v.vec16, tiles32 = p.k.tile && p.v.tile && !(my_table && p.page_rows & 31);
+    const uint32_t head_rows = (uint32_t)p.Hkv * (uint32_t)p.page_rows, my_rows = (uint32_t)kvh * (uint32_t)p.page_rows;
     const int mask = p.page_shift >= 0 ? p.page_rows - 1 : 0;
     auto page_of = [&](int tok) -> int {          // the page holding middle token tok, -1: none
       if (tok >= sq.nm) return -1;
@@ -385,13 +390,16 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
     };
     auto row_in_page = [&](int tok) -> int { return !my_table ? tok : p.page_shift >= 0 ? tok & mask : tok % p.page_rows; };
     uint32_t partial = 0;                         // bit i % 32: tile i does not hold 32 tokens (which it holds: vms)
+    const bool split_tiles = my_table && (p.page_rows & 31);   // a tile may lie in two pages
     auto issue = [&](int i, int st, int pg0, int pg1) {
       const int tok = (t_first + i * kKaWarps) * kKaTile;
       const uint32_t so = st * Sh::kStageBytes;
-      const int r0 = row_in_page(tok), r1 = row_in_page(tok + 16);
-      const uint32_t row0 = (uint32_t)pg0 * head_rows + my_rows + r0, row1 = (uint32_t)pg1 * head_rows + my_rows + r1;
+      const int r0 = row_in_page(tok), r1 = split_tiles ? row_in_page(tok + 16) : r0 + 16;
+      const uint32_t row0 = (uint32_t)pg0 * head_rows + my_rows + r0;
+      const uint32_t row1 = split_tiles ? (uint32_t)pg1 * head_rows + my_rows + r1 : row0 + 16;
       const bool whole = (pg0 | pg1) >= 0 && tok + kKaTile <= sq.nm;
-      if (whole && pieces16) {
+      uint32_t vm = 0xFFFFFFFFu;
+      if (whole) {
         const uint8_t *k0 = kc + (uint64_t)row0 * Sh::kCodeRow, *k1 = kc + (uint64_t)row1 * Sh::kCodeRow;
         const uint8_t *v0 = vc + (uint64_t)row0 * Sh::kCodeRow, *v1 = vc + (uint64_t)row1 * Sh::kCodeRow;
 #pragma unroll
@@ -400,29 +408,40 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
           cp_async16(ka + so + it * 512, (it < HALF ? k0 : k1) + (it % HALF) * 512);
           cp_async16(v_at + so + it * 512, (it < HALF ? v0 : v1) + (it % HALF) * 512);
         }
-        const uint32_t sa = ring_u + so + Sh::kKS + lane * 16;
-        if constexpr (NP == 32) {
-          const uint64_t o = (uint64_t)(lane < 16 ? row0 : row1) * Sh::kScaleRow;
-          cp_async16(sa, sc + o);
-          cp_async16(sa + Sh::kVS - Sh::kKS, sc + (p.v.scales - p.k.scales) + o);
-        } else if (lane < 2 * NP) {
-          cp_async16(sa, sc + (uint64_t)(lane % NP < NP / 2 ? row0 : row1) * Sh::kScaleRow);
+        const uint32_t sa = ring_u + so + Sh::kKS;
+        if (pieces16) {
+          if constexpr (NP == 32) {
+            const uint64_t o = (uint64_t)(lane < 16 ? row0 : row1) * Sh::kScaleRow;
+            cp_async16(sa + lane * 16, sc + o);
+            cp_async16(sa + lane * 16 + Sh::kVS - Sh::kKS, sc + (p.v.scales - p.k.scales) + o);
+          } else if (lane < 2 * NP) {
+            cp_async16(sa + lane * 16, sc + (uint64_t)(lane % NP < NP / 2 ? row0 : row1) * Sh::kScaleRow);
+          }
+          return;
         }
-        return;
-      }
-      const int n0 = pg0 >= 0 ? min(max(sq.nm - tok, 0), 16) : 0, n1 = pg1 >= 0 ? min(max(sq.nm - tok - 16, 0), 16) : 0;
-      const uint32_t vm = ((1u << n0) - 1u) | ((1u << n1) - 1u) << 16;
-      if (!whole) {
+        if (tiles32 && (r0 & 31) == 0) {          // 32 rows of a scale tile: every fourth word of its 512 bytes
+          const uint64_t o = (uint64_t)((uint32_t)pg0 * (uint32_t)p.Hkv + kvh) * p.k.mat_bytes + (uint32_t)(r0 >> 7) * (D / 64 * 512) +
+                             4 * (r0 >> 5 & 3) + lane * 16;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            cp_async4(sa + lane * Sh::kScaleRow + 4 * j, p.k.scales + o + j * 512);
+            cp_async4(sa + Sh::kVS - Sh::kKS + lane * Sh::kScaleRow + 4 * j, p.v.scales + o + j * 512);
+          }
+          return;
+        }
+      } else {
+        const int n0 = pg0 >= 0 ? min(max(sq.nm - tok, 0), 16) : 0, n1 = pg1 >= 0 ? min(max(sq.nm - tok - 16, 0), 16) : 0;
+        vm = ((1u << n0) - 1u) | ((1u << n1) - 1u) << 16;
         partial |= 1u << (i & 31);
         if (lane == 0) vms[w * ST + st] = vm;
-      }
 #pragma unroll
-      for (int it = 0; it < ITS; ++it) {
-        const int ok = vm >> (it * (32 / CPR) + lane_row) & 1u;
-        const uint64_t o = ok ? (uint64_t)(it < HALF ? row0 : row1) * Sh::kCodeRow + (it % HALF) * 512 : 0;
-        const uint32_t ka = D == 256 ? k_at ^ (uint32_t)(it & 1) << 6 : k_at;
-        cp_async16(ka + so + it * 512, kc + o, ok ? 16 : 0);
-        cp_async16(v_at + so + it * 512, vc + o, ok ? 16 : 0);
+        for (int it = 0; it < ITS; ++it) {
+          const int ok = vm >> (it * (32 / CPR) + lane_row) & 1u;
+          const uint64_t o = ok ? (uint64_t)(it < HALF ? row0 : row1) * Sh::kCodeRow + (it % HALF) * 512 : 0;
+          const uint32_t ka = D == 256 ? k_at ^ (uint32_t)(it & 1) << 6 : k_at;
+          cp_async16(ka + so + it * 512, kc + o, ok ? 16 : 0);
+          cp_async16(v_at + so + it * 512, vc + o, ok ? 16 : 0);
+        }
       }
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
@@ -443,11 +462,12 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
         }
       }
     };
-    int next[2];                                  // pages of the tile that is issued next
+    int next[2] = {-1, -1};                       // pages of the tile that is issued next
     auto look_up = [&](int i) {
+      if (i >= n_my) return;
       const int tok = (t_first + i * kKaWarps) * kKaTile;
-      next[0] = i < n_my ? page_of(tok) : -1;
-      next[1] = i < n_my ? page_of(tok + 16) : -1;
+      next[0] = page_of(tok);
+      next[1] = split_tiles ? page_of(tok + 16) : next[0];
     };
     look_up(0);
 #pragma unroll
@@ -501,18 +521,18 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
       constexpr int CD = D >= 128 ? 32 : 16;
       const int c0 = blk * 16, chunk = c0 / CD, ft = chunk & 3, j0 = (chunk >> 2) * 8 + (c0 % CD) / 4;
       const int fl = (row & 7) * 4 + ft, nt = row >> 3;
-      uint4* eo = qe + (nt * NS + j0) * 32 + fl;
-      uint4* fo = qf + (nt * NS + j0) * 32 + fl;
+      const int fo = (nt * NS + j0) * 32 + fl;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint4 v;
         if constexpr (QBF) {
-          v = make_uint4(pack_bf16(a[4 * j], a[4 * j + 1]), pack_bf16(a[4 * j + 2], a[4 * j + 3]), 0u, 0u);
+          qe[fo + j * 32] = make_uint2(pack_bf16(a[4 * j], a[4 * j + 1]), pack_bf16(a[4 * j + 2], a[4 * j + 3]));
         } else {
+          uint4 v;
           split_bf16(a[4 * j], a[4 * j + 1], v.x, v.z);
           split_bf16(a[4 * j + 2], a[4 * j + 3], v.y, v.w);
+          qe[fo + j * 32] = make_uint2(v.x, v.y);
+          qr[fo + j * 32] = make_uint2(v.z, v.w);
         }
-        eo[j * 32] = v;
       }
       if (p.k.rotate) fwht16(a);
       const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;            // carried by the query, so that factors are >= 0
@@ -529,7 +549,7 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
         uint4 v;
         split_f16(a[4 * j] * down, a[4 * j + 1] * down, v.x, v.z);
         split_f16(a[4 * j + 2] * down, a[4 * j + 3] * down, v.y, v.w);
-        fo[j * 32] = v;
+        qf[fo + j * 32] = v;
       }
       if (blk == 0) {
         rowfac[row] = __uint_as_float((uint32_t)(127 + e) << 23);
@@ -601,55 +621,61 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
         fac[n][1] *= gk;
       }
     }
+    // A lane's offsets in a stage: rows are added as constants (the exchanges of halves depend on bits of the row
+    // that those constants leave alone).
+    const int k_read = Sh::kKC + ((perm * Sh::kCodeRow + t * (KW * 4)) ^ (perm >> 2 & 1) << 6);
+    const int k_read2 = Sh::kKC + ((perm * Sh::kCodeRow + (t + 4) * (KW * 4)) ^ (perm >> 2 & 1) << 6);   // D = 256
+    const int v_read = Sh::kVC + ((t * Sh::kCodeRow + g * (VW * 4)) ^ (D == 256 ? t << 5 : D == 128 ? (t >> 1 & 1) << 5 : 0));
+    const int ks_read = Sh::kKS + perm * Sh::kScaleRow + (KW == 4 ? 2 * t : t);
+    const int vs_read = Sh::kVS + t * Sh::kScaleRow + (D == 256 ? 2 * g : D == 128 ? g : g >> 1);
+
     // One tile of 32 tokens.  FULL: all of them exist and every row sees them.
     auto work = [&](auto full, const unsigned char* st, int tok0, uint32_t vm) {
       constexpr bool FULL = decltype(full)::value;
       // ---- S^T = K Q^T: rows are tokens (two tiles of 16), columns query rows ----
       float S[2][NT][4];
 #pragma unroll
-      for (int cc = 0; cc < KCH; ++cc) {
-        uint32_t kw[4][KW], ks[4][KW / 2];         // rows perm + 8 k of the tile; scales doubled into both halves
+      for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = perm + 8 * k;
-          const uint32_t sw = ((uint32_t)row >> 2 & 1u) << 6;
-          if constexpr (KW == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kKC + ((row * Sh::kCodeRow + (t + 4 * cc) * 16) ^ sw));
-            kw[k][0] = v.x, kw[k][1] = v.y, kw[k][2] = v.z, kw[k][3] = v.w;
-            const uint32_t h = e4m3x2_f16x2(*reinterpret_cast<const unsigned short*>(st + Sh::kKS + row * Sh::kScaleRow + 2 * t + 8 * cc));
-            ks[k][0] = both_lo(h);
-            ks[k][1] = both_hi(h);
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kKC + ((row * Sh::kCodeRow + t * 8) ^ sw));
-            kw[k][0] = v.x, kw[k][1] = v.y;
-            ks[k][0] = both_lo(e4m3x2_f16x2(st[Sh::kKS + row * Sh::kScaleRow + t]));
-          }
-        }
+        for (int cc = 0; cc < KCH; ++cc) {
+          uint32_t kw[2][KW], ks[2][KW / 2];     // rows perm and perm + 8; scales doubled into both halves
 #pragma unroll
-        for (int wd = 0; wd < KW; ++wd) {          // a word of 8 codes feeds two steps
-          uint32_t h[4][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            e2m1x8(kw[k][wd], h[k]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) h[k][c] = hmul2(h[k][c], ks[k][wd >> 1]);
+          for (int k = 0; k < 2; ++k) {
+            const int row = 8 * k + 16 * a;      // + perm, in the lane's offsets
+            if constexpr (KW == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(st + (cc ? k_read2 : k_read) + row * Sh::kCodeRow);
+              kw[k][0] = v.x, kw[k][1] = v.y, kw[k][2] = v.z, kw[k][3] = v.w;
+              const uint32_t h = e4m3x2_f16x2(*reinterpret_cast<const unsigned short*>(st + ks_read + row * Sh::kScaleRow + 8 * cc));
+              ks[k][0] = both_lo(h);
+              ks[k][1] = both_hi(h);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(st + k_read + row * Sh::kCodeRow);
+              kw[k][0] = v.x, kw[k][1] = v.y;
+              ks[k][0] = both_lo(e4m3x2_f16x2(st[ks_read + row * Sh::kScaleRow]));
+            }
           }
 #pragma unroll
-          for (int j2 = 0; j2 < 2; ++j2) {
-            const int j = cc * 8 + wd * 2 + j2;
+          for (int wd = 0; wd < KW; ++wd) {      // a word of 8 codes feeds two steps
+            uint32_t h[2][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 qv = qf[(n * NS + j) * 32 + lane];
+            for (int k = 0; k < 2; ++k) {
+              e2m1x8(kw[k][wd], h[k]);
 #pragma unroll
-              for (int a = 0; a < 2; ++a) {
-                if (j == 0) mma16816_zero(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
-                else mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.x, qv.y);
-                mma16816<false>(S[a][n], h[2 * a][2 * j2], h[2 * a + 1][2 * j2], h[2 * a][2 * j2 + 1], h[2 * a + 1][2 * j2 + 1], qv.z, qv.w);
+              for (int c = 0; c < 4; ++c) h[k][c] = hmul2(h[k][c], ks[k][wd >> 1]);
+            }
+#pragma unroll
+            for (int j2 = 0; j2 < 2; ++j2) {
+              const int j = cc * 8 + wd * 2 + j2;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint4 qv = qf[(n * NS + j) * 32 + lane];
+                if (j == 0) mma16816_zero(S[a][n], h[0][2 * j2], h[1][2 * j2], h[0][2 * j2 + 1], h[1][2 * j2 + 1], qv.x, qv.y);
+                else mma16816<false>(S[a][n], h[0][2 * j2], h[1][2 * j2], h[0][2 * j2 + 1], h[1][2 * j2 + 1], qv.x, qv.y);
+                mma16816<false>(S[a][n], h[0][2 * j2], h[1][2 * j2], h[0][2 * j2 + 1], h[1][2 * j2 + 1], qv.z, qv.w);
               }
             }
           }
         }
-      }
       // ---- numerators (fac >= 0: maxima are taken before it is applied) ----
       float mx[NT][2];
 #pragma unroll
@@ -691,28 +717,27 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
         uint32_t vw[4][VW], vs[2][VB];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * a + 4 * r + t;
+          const int row = 16 * a + 4 * r;        // + t, in the lane's offset
           if constexpr (VW == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(st + Sh::kVC + ((row * Sh::kCodeRow + g * 16) ^ ((row & 3) << 5)));
+            const uint4 v = *reinterpret_cast<const uint4*>(st + v_read + row * Sh::kCodeRow);
             vw[r][0] = v.x, vw[r][1] = v.y, vw[r][2] = v.z, vw[r][3] = v.w;
           } else if constexpr (VW == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(st + Sh::kVC + ((row * Sh::kCodeRow + g * 8) ^ ((row >> 1 & 1) << 5)));
+            const uint2 v = *reinterpret_cast<const uint2*>(st + v_read + row * Sh::kCodeRow);
             vw[r][0] = v.x, vw[r][1] = v.y;
           } else {
-            vw[r][0] = *reinterpret_cast<const uint32_t*>(st + Sh::kVC + row * Sh::kCodeRow + g * 4);
+            vw[r][0] = *reinterpret_cast<const uint32_t*>(st + v_read + row * Sh::kCodeRow);
           }
         }
 #pragma unroll
         for (int q2 = 0; q2 < 2; ++q2) {
-          const unsigned char* s0 = st + Sh::kVS + (16 * a + 8 * q2 + t) * Sh::kScaleRow;
+          const unsigned char* s0 = st + vs_read + (16 * a + 8 * q2) * Sh::kScaleRow;
           const unsigned char* s1 = s0 + 4 * Sh::kScaleRow;
           if constexpr (VB == 2) {
-            const uint32_t u0 = *reinterpret_cast<const unsigned short*>(s0 + 2 * g), u1 = *reinterpret_cast<const unsigned short*>(s1 + 2 * g);
+            const uint32_t u0 = *reinterpret_cast<const unsigned short*>(s0), u1 = *reinterpret_cast<const unsigned short*>(s1);
             vs[q2][0] = e4m3x2_f16x2(__byte_perm(u0, u1, 0x0040));
             vs[q2][1] = e4m3x2_f16x2(__byte_perm(u0, u1, 0x0051));
           } else {
-            const int blk = D == 128 ? g : g >> 1;
-            vs[q2][0] = e4m3x2_f16x2(s0[blk] | (uint32_t)s1[blk] << 8);
+            vs[q2][0] = e4m3x2_f16x2(__byte_perm(*s0, *s1, 0x0040));
           }
         }
         uint32_t nan_tok[VB];
@@ -880,12 +905,12 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
           const int j = cc * 8 + v8 * 2;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint4 qa = qe[(n * NS + j) * 32 + lane], qb = qe[(n * NS + j + 1) * 32 + lane];
-            mma16816<true>(S[n], u.x, v.x, u.y, v.y, qa.x, qa.y);
-            mma16816<true>(S[n], u.z, v.z, u.w, v.w, qb.x, qb.y);
-            if constexpr (!QBF) {                  // a BF16 query is its first term
-              mma16816<true>(S[n], u.x, v.x, u.y, v.y, qa.z, qa.w);
-              mma16816<true>(S[n], u.z, v.z, u.w, v.w, qb.z, qb.w);
+            const int at = (n * NS + j) * 32 + lane;
+            mma16816<true>(S[n], u.x, v.x, u.y, v.y, qe[at].x, qe[at].y);
+            mma16816<true>(S[n], u.z, v.z, u.w, v.w, qe[at + 32].x, qe[at + 32].y);
+            if constexpr (!QBF) {
+              mma16816<true>(S[n], u.x, v.x, u.y, v.y, qr[at].x, qr[at].y);
+              mma16816<true>(S[n], u.z, v.z, u.w, v.w, qr[at + 32].x, qr[at + 32].y);
             }
           }
         }
