@@ -753,14 +753,21 @@ def attention_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: boo
 
 
 # ---- decode: attention over the cache, rotary positions, cache pages ----
+# the current stream's handle without a Stream object around it (5 us per call), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _launch(device: torch.device, fn, *args) -> None:
     """fn(*args, stream) on `device` and its current stream: a kernel is launched on the current device, so
     that one is switched when the tensors live on another."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    i = device.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+            rc = fn(*args, _raw_stream(i))
+    if rc:
+        raise NVFP4Error(rc)
 
 
 def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -1034,48 +1041,60 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
     xs = [x] if one else list(x)
     if not xs or len(xs) > ROPE_MAX:
         raise ValueError(f"1 to {ROPE_MAX} tensors per call")
-    x0 = xs[0]
-    dev, dt = _rows(x0, "x").device, _dt(x0)
-    outs = [None] * len(xs) if out is None else [out] if one else list(out)
+    given = out is not None
+    outs = ([out] if one else list(out)) if given else [None] * len(xs)
     if len(outs) != len(xs):
         raise ValueError("one output per tensor")
-    nd = x0.dim()
+    x0 = _rows(xs[0], "x")
+    dev, dtype, dt, nd = x0.device, x0.dtype, _dt(x0), x0.dim()
     if nd not in (3, 4):
         raise ValueError("x must be [B, heads, T, D] or [heads, T, D]")
-    B, T, D = x0.shape[0] if nd == 4 else 1, x0.shape[-2], x0.shape[-1]
+    s0 = x0.shape
+    B, T, D = s0[0] if nd == 4 else 1, s0[-2], s0[-1]
     _cuda(freqs, "freqs")
     if freqs.dtype != torch.float64 or freqs.dim() != 1 or freqs.device != dev:
         raise TypeError("freqs must be a 1-D float64 tensor on x's device")
     rot = 2 * freqs.shape[0]
     if rot > D:
         raise ValueError("freqs holds more pairs than x has channels")
-    if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype not in (torch.int32, torch.int64):
+    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64) or not positions.is_cuda:
         raise TypeError("positions must be an int32 or int64 CUDA tensor")
-    if positions.shape not in ((T,), (B, T)) or positions.device != dev:
+    pos_shape, ps = positions.shape, positions.stride()
+    if pos_shape not in ((T,), (B, T)) or positions.device != dev:
         raise ValueError("positions must be [T] or [B, T] on x's device")
-    ps = positions.stride()
     descs = (_RopeTensor * len(xs))()
-    for j, (a, o) in enumerate(zip(xs, outs)):
-        _rows(a, "x")
-        if a.dim() != nd or a.shape[-2:] != (T, D) or (nd == 4 and a.shape[0] != B) or a.dtype != x0.dtype or a.device != dev:
-            raise ValueError("the tensors of a call share batch, length, head_dim, dtype and device")
-        if o is None:
-            o = outs[j] = torch.empty(a.shape, dtype=a.dtype, device=dev)
+    for j, a in enumerate(xs):
+        if j:
+            _rows(a, "x")
+            s = a.shape
+            if len(s) != nd or s[-2] != T or s[-1] != D or (nd == 4 and s[0] != B) or a.dtype != dtype or a.device != dev:
+                raise ValueError("the tensors of a call share batch, length, head_dim, dtype and device")
         else:
-            _rows(o, "out")
-            if o.shape != a.shape or o.dtype != a.dtype or o.device != dev:
+            s = s0
+        sx = a.stride()
+        if not given:
+            o = outs[j] = torch.empty(s, dtype=dtype, device=dev)
+        else:
+            o = _rows(outs[j], "out")
+            if o.shape != s or o.dtype != dtype or o.device != dev:
                 raise ValueError("out must have x's shape, dtype and device")
             _no_shared_elements(o, "out")
             if any(o.data_ptr() == outs[i].data_ptr() and o.numel() for i in range(j)):
                 raise ValueError("two outputs are the same tensor")
-            if not (o.data_ptr() == a.data_ptr() and o.stride() == a.stride()) and any(_overlap(o, b) for b in xs):
+            if not (o.data_ptr() == a.data_ptr() and o.stride() == sx) and any(_overlap(o, b) for b in xs):
                 raise ValueError("out must be x itself or not overlap any x")
-        sx, so = a.stride(), o.stride()
-        descs[j] = _RopeTensor(a.data_ptr(), o.data_ptr(), a.shape[-3], sx[0] if nd == 4 else 0, sx[-3], sx[-2],
-                               so[0] if nd == 4 else 0, so[-3], so[-2])
-    _launch(dev, lib().nvfp4_rope, descs, len(xs), B, T, D, rot, int(bool(interleaved)), dt, positions.data_ptr(),
-            int(positions.dtype == torch.int64), ps[0] if len(ps) == 2 else 0, ps[-1], freqs.data_ptr(), float(mscale),
-            int(bool(inverse)))
+        so = o.stride()
+        d = descs[j]
+        d.x, d.out, d.heads = a.data_ptr(), o.data_ptr(), s[-3]
+        if nd == 4:
+            d.x_sb, d.x_sh, d.x_st, _ = sx
+            d.out_sb, d.out_sh, d.out_st, _ = so
+        else:
+            d.x_sh, d.x_st, _ = sx
+            d.out_sh, d.out_st, _ = so
+    _launch(dev, lib().nvfp4_rope, descs, len(xs), B, T, D, rot, 1 if interleaved else 0, dt, positions.data_ptr(),
+            1 if positions.dtype == torch.int64 else 0, ps[0] if len(ps) == 2 else 0, ps[-1], freqs.data_ptr(), mscale,
+            1 if inverse else 0)
     return outs[0] if one else outs
 
 
@@ -1110,7 +1129,8 @@ def copy_pages(arrays, src, dst) -> None:
         outer, pages = math.prod(t.shape[:dim]), t.shape[dim]
         item = math.prod(t.shape[dim + 1:]) * t.element_size()
         descs[j] = _PagesArray(t.data_ptr(), outer, pages * item, item, pages)
-    if any(a[0].numel() and b[0].numel() and _overlap(a[0], b[0]) for i, a in enumerate(arrays) for b in arrays[:i]):
+    spans = sorted((d.base, d.base + d.outer * d.stride) for d in descs if d.outer * d.stride)
+    if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
         raise ValueError("two arrays overlap")
     s, d = (array.array("i", list(v)) for v in (src, dst))
     _launch(dev, lib().nvfp4_copy_pages, descs, len(arrays), s.buffer_info()[0], d.buffer_info()[0], len(s))

@@ -207,7 +207,7 @@ int nvfp4_rope(const nvfp4_rope_tensor* tensors, int count, int64_t B, int64_t T
   if (count < 0 || count > kRopeMaxTensors || (count > 0 && tensors == nullptr) || !dtype_ok(dtype) ||
       (interleaved != 0 && interleaved != 1) || (positions64 != 0 && positions64 != 1) || (inverse != 0 && inverse != 1))
     return NVFP4_ERR_ARG;
-  if (B < 0 || T < 0 || D < 0 || rot < 0 || rot > D || rot % 2 != 0 || rot / 2 > kRopeMaxPairs || D > kMaxInt ||
+  if (B < 0 || T < 0 || D < 0 || rot < 0 || rot > D || rot % 2 != 0 || rot / 2 > kRopeMaxPairs || D > kMaxInt || T > kMaxInt / 2 ||
       checked_prod({B, T}) < 0)
     return NVFP4_ERR_SIZE;
   RopeParams p{};
@@ -233,8 +233,7 @@ int nvfp4_rope(const nvfp4_rope_tensor* tensors, int count, int64_t B, int64_t T
   if (!aligned(positions, positions64 ? 8 : 4) || !aligned(freqs, 8)) return NVFP4_ERR_ALIGN;
   if (heads > kMaxInt / 4096) return NVFP4_ERR_SIZE;   // (token, head) rows of a CTA are counted in 32 bits
   p.heads = (int)heads;
-  p.tokens = B * T;
-  p.T = T;
+  p.T = (int)T;
   p.D = (int)D;
   p.rot = (int)rot;
   p.interleaved = interleaved;
@@ -251,12 +250,13 @@ int nvfp4_rope(const nvfp4_rope_tensor* tensors, int count, int64_t B, int64_t T
   const int64_t half = rot / 2, pieces = (interleaved ? rot : half) / v + (D - rot) / v;
   const int64_t per_pass = std::max<int64_t>(1, kRopeThreads / std::max<int64_t>(1, pieces));
   const int sms = sm_count();
-  // tokens per CTA: as many as leave four CTAs per SM, up to 8 passes of its threads over (token, head) rows
+  // tokens per CTA (of one sequence): as many as leave two CTAs per SM, up to 32 passes of its threads over (token, head) rows
   int64_t tile = 1;
-  while (tile < 32 && 2 * tile * half <= kRopeSmemPairs && p.tokens / (2 * tile) >= 4 * sms && 2 * tile * heads <= 8 * per_pass)
+  while (tile < 32 && 2 * tile * half <= kRopeSmemPairs && tile < T && B * T / (2 * tile) >= 2 * sms && 2 * tile * heads <= 32 * per_pass)
     tile *= 2;
   p.tile = (int)tile;
-  const int64_t gx = (p.tokens + tile - 1) / tile;
+  p.tiles = (int)((T + tile - 1) / tile);
+  const int64_t gx = B * p.tiles;
   if (gx > kMaxInt) return NVFP4_ERR_SIZE;
   // few tokens (a decode step): the heads of a token are shared among CTAs until there are two per SM
   const int64_t passes = (tile * heads + per_pass - 1) / per_pass;

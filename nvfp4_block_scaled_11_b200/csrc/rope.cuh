@@ -28,8 +28,8 @@ struct RopeTensor {
 struct RopeParams {
   RopeTensor a[kRopeMaxTensors];
   int count, heads;                        // tensors; heads of all of them
-  int64_t tokens, T;                       // B * T; token j is (j / T, j % T)
-  int D, rot, interleaved, pos64, tile;    // tile: tokens per CTA
+  int T, tiles;                            // tokens of a sequence, and the CTAs that share them
+  int D, rot, interleaved, pos64, tile;    // tile: tokens per CTA (of one sequence)
   const void* pos;                         // int32 / int64, element b * pos_b + t * pos_t
   int64_t pos_b, pos_t;
   const double* freqs;                     // rot / 2
@@ -48,19 +48,30 @@ __device__ __forceinline__ void rope_narrow(char* p, int64_t i, float x) {
   else if (DT == DT_BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
   else reinterpret_cast<__half*>(p)[i] = __float2half_rn(x);
 }
-// V consecutive elements: one 16-byte access (V = 16 / size) or V single ones.  Plain loads, since `out`
-// may be x itself.
+// V consecutive elements as they lie: one 16-byte access (V = 16 / size), or V single ones.  Plain loads, since `out` may
+// be x itself.
 template <int DT, int V, bool VEC>
-__device__ __forceinline__ void rope_load(const char* p, int64_t i, float (&f)[V]) {
-  if constexpr (VEC) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p + i * (16 / V));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    widen_words<DT>(w, f, 4);
-  } else {
+struct RopePiece {
+  uint4 raw;
+  float one[VEC ? 1 : V];
+  __device__ __forceinline__ void load(const char* p, int64_t i) {
+    if constexpr (VEC) {
+      raw = *reinterpret_cast<const uint4*>(p + i * (16 / V));
+    } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = rope_widen<DT>(p, i + k);
+      for (int k = 0; k < V; ++k) one[k] = rope_widen<DT>(p, i + k);
+    }
   }
-}
+  __device__ __forceinline__ void widen(float (&f)[V]) const {
+    if constexpr (VEC) {
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      widen_words<DT>(w, f, 4);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = one[k];
+    }
+  }
+};
 template <int DT, int V, bool VEC>
 __device__ __forceinline__ void rope_store(char* p, int64_t i, const float (&f)[V]) {
   if constexpr (VEC) {
@@ -88,75 +99,98 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   constexpr int V = VEC ? (DT == DT_F32 ? 4 : 8) : (INTER ? 2 : 1);   // elements per piece
   constexpr int PP = INTER ? V / 2 : V;                               // pairs per piece (divides rot / 2)
   __shared__ float2 cs[kRopeSmemPairs];
+  constexpr int ES = DT == DT_F32 ? 4 : 2, U = INTER ? 2 : 1;          // rows per step (a row of the half layout is two loads)
   const int half = p.rot / 2, tid = threadIdx.x;
-  const int64_t tok0 = (int64_t)blockIdx.x * p.tile;
-  const int ntok = (int)min((int64_t)p.tile, p.tokens - tok0);
-  for (int u = tid; u < ntok * half; u += kRopeThreads) {
-    const int j = u / half, i = u - j * half;
-    const int64_t tok = tok0 + j, b = tok / p.T, at = b * p.pos_b + (tok - b * p.T) * p.pos_t;
-    const double pos = p.pos64 ? (double)reinterpret_cast<const long long*>(p.pos)[at]
-                               : (double)reinterpret_cast<const int*>(p.pos)[at];
-    const double turns = pos * p.freqs[i] * 0.15915494309189535;   // / (2 pi)
-    float s, c;
-    sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-    // kept so that the pairs of neighbouring pieces lie side by side (threads of a warp read those together)
-    cs[j * half + (i % PP) * (half / PP) + i / PP] = make_float2(c * p.mscale, s * (p.mscale * p.sign));
+  const int seq = blockIdx.x / p.tiles, t0 = (blockIdx.x - seq * p.tiles) * p.tile, ntok = min(p.tile, p.T - t0);
+  __shared__ const char* xs[kRopeMaxTensors];                             // the tensors' first rows of this CTA
+  __shared__ char* os[kRopeMaxTensors];
+  if (tid < p.count) {
+    xs[tid] = p.a[tid].x + (seq * p.a[tid].xb + t0 * p.a[tid].xt) * ES;
+    os[tid] = p.a[tid].out + (seq * p.a[tid].ob + t0 * p.a[tid].ot) * ES;
   }
   __syncthreads();
   // pieces of a row: pairs first (two pieces in the half layout), then the channels that pass
   const int turning = INTER ? p.rot / V : half / V, pieces = turning + (p.D - p.rot) / V;
-  const int64_t total = (int64_t)pieces;
-  for (int64_t pc0 = 0; pc0 < total; pc0 += kRopeThreads) {   // rows of more than 256 pieces take several rounds
-    const int width = (int)min((int64_t)kRopeThreads, total - pc0), rows = kRopeThreads / width;
-    if (tid >= rows * width) continue;
-    const int pc = (int)pc0 + tid % width;
-    int row = tid / width + (int)blockIdx.y * rows, h, tok;
-    const int step = rows * (int)gridDim.y;
-    tok = row / p.heads;
-    h = row - tok * p.heads;
+  bool ready = false;
+  for (int pc0 = 0; pc0 < pieces || !ready; pc0 += kRopeThreads) {      // rows of more than 256 pieces take several rounds
+    const int width = max(min(kRopeThreads, pieces - pc0), 1), rows = kRopeThreads / width;
+    const int pc = pc0 + tid % width, step = rows * (int)gridDim.y, first = tid / width + (int)blockIdx.y * rows;
+    int tok = tid < rows * width && pc0 < pieces ? first / p.heads : ntok, h = first % p.heads;
     const int dt = step / p.heads, dh = step - dt * p.heads;
-    for (; tok < ntok; tok += dt, h += dh) {
-      if (h >= p.heads) {
-        h -= p.heads;
-        if (++tok >= ntok) break;
-      }
-      int k = 0, hh = h;
-      while (hh >= p.a[k].heads) hh -= p.a[k++].heads;
-      const RopeTensor& a = p.a[k];
-      const int64_t g = tok0 + tok, b = g / p.T, t = g - b * p.T;
-      const char* x = a.x + (b * a.xb + hh * a.xh + t * a.xt) * (DT == DT_F32 ? 4 : 2);
-      char* o = a.out + (b * a.ob + hh * a.oh + t * a.ot) * (DT == DT_F32 ? 4 : 2);
-      const float2* c = cs + tok * half;
-      if (pc >= turning) {
-        const int at = p.rot + (pc - turning) * V;
-        float f[V];
-        rope_load<DT, V, VEC>(x, at, f);
-        rope_store<DT, V, VEC>(o, at, f);
-      } else if constexpr (INTER) {
-        float f[V];
-        rope_load<DT, V, VEC>(x, pc * V, f);
+    const bool turns = pc < turning;
+    const int at = turns ? pc * V : p.rot + (pc - turning) * V;          // the piece's first channel
+    struct Rows {
+      char* o[U];                                                        // null: no row
+      const float2* c[U];
+      RopePiece<DT, V, VEC> f[U], s[U];
+    } cur;
+    auto fetch = [&](Rows& n) {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          const float2 r = c[i * (half / PP) + pc];
-          const float u = f[2 * i], v = f[2 * i + 1];
-          f[2 * i] = u * r.x - v * r.y;
-          f[2 * i + 1] = u * r.y + v * r.x;
-        }
-        rope_store<DT, V, VEC>(o, pc * V, f);
-      } else {
-        float f[V], s[V];
-        rope_load<DT, V, VEC>(x, pc * V, f);
-        rope_load<DT, V, VEC>(x, half + pc * V, s);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 r = c[i * (half / PP) + pc];
-          const float u = f[i], v = s[i];
-          f[i] = u * r.x - v * r.y;
-          s[i] = u * r.y + v * r.x;
-        }
-        rope_store<DT, V, VEC>(o, pc * V, f);
-        rope_store<DT, V, VEC>(o, half + pc * V, s);
+      for (int u = 0; u < U; ++u) {
+        n.o[u] = nullptr;
+        if (tok >= ntok) continue;
+        int k = 0, hh = h;
+        while (hh >= p.a[k].heads) hh -= p.a[k++].heads;
+        const RopeTensor& a = p.a[k];
+        const char* x = xs[k] + (hh * a.xh + tok * a.xt) * ES;
+        n.o[u] = os[k] + (hh * a.oh + tok * a.ot) * ES;
+        n.c[u] = cs + tok * half;
+        n.f[u].load(x, at);
+        if (!INTER && turns) n.s[u].load(x, half + at);
+        tok += dt;
+        h += dh;
+        if (h >= p.heads) h -= p.heads, ++tok;
       }
+    };
+    fetch(cur);
+    if (!ready) {                                                        // while the first rows are on their way
+      const int lanes = max(min(half, kRopeThreads), 1), abreast = kRopeThreads / lanes, i0 = tid % lanes;
+      for (int j = tid < lanes * abreast ? tid / lanes : ntok; j < ntok; j += abreast) {
+        const int64_t pos_at = seq * p.pos_b + (t0 + j) * p.pos_t;
+        const double pos = p.pos64 ? (double)reinterpret_cast<const long long*>(p.pos)[pos_at]
+                                   : (double)reinterpret_cast<const int*>(p.pos)[pos_at];
+        for (int i = i0; i < half; i += lanes) {
+          const double turn = pos * p.freqs[i] * 0.15915494309189535;    // / (2 pi)
+          float s, c;
+          sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
+          // kept so that the pairs of neighbouring pieces lie side by side (threads of a warp read those together)
+          cs[j * half + (i % PP) * (half / PP) + i / PP] = make_float2(c * p.mscale, s * (p.mscale * p.sign));
+        }
+      }
+      __syncthreads();
+      ready = true;
+    }
+    while (cur.o[0] != nullptr) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (cur.o[u] == nullptr) continue;
+        float f[V];
+        cur.f[u].widen(f);
+        if (turns) {
+          if constexpr (INTER) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+              const float2 r = cur.c[u][i * (half / PP) + pc];
+              const float a = f[2 * i], b = f[2 * i + 1];
+              f[2 * i] = a * r.x - b * r.y;
+              f[2 * i + 1] = a * r.y + b * r.x;
+            }
+          } else {
+            float s[V];
+            cur.s[u].widen(s);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float2 r = cur.c[u][i * (half / PP) + pc];
+              const float a = f[i], b = s[i];
+              f[i] = a * r.x - b * r.y;
+              s[i] = a * r.y + b * r.x;
+            }
+            rope_store<DT, V, VEC>(cur.o[u], half + at, s);
+          }
+        }
+        rope_store<DT, V, VEC>(cur.o[u], at, f);
+      }
+      fetch(cur);
     }
   }
 }
