@@ -203,6 +203,12 @@ __device__ __forceinline__ void split_bf16(float lo, float hi, uint32_t& a, uint
   a = pack_bf16(h0, h1);
   b = pack_bf16(r0, r1);
 }
+// a bf16x2 with halves that are infinite or NaN replaced by zero
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t u) {
+  if ((u & 0x7F80u) == 0x7F80u) u &= 0xFFFF0000u;
+  if ((u & 0x7F800000u) == 0x7F800000u) u &= 0x0000FFFFu;
+  return u;
+}
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // The lengths of the sequence of batch row b, bounded by the buffers (an unknown slot is an empty sequence).
@@ -601,7 +607,8 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xFFFFFFFFu, mx[n][c], o));
-          const float mn = fmaxf(m[n][c], mx[n][c]);
+          // (each row by its own scores alone: what other rows see changes no bit of it)
+          const float mn = mx[n][c] > m[n][c] + kKaSlack ? mx[n][c] : m[n][c];
           const float al = ex2(m[n][c] - finite_or_zero(mn));
           m[n][c] = mn;
           l[n][c] *= al;
@@ -959,21 +966,28 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
           vv[r] = make_uint4(0, 0, 0, 0);
           if (ok) vv[r] = *reinterpret_cast<const uint4*>(row_at(p.v, 4 * r + t) + (g * (D / 8) + v8 * 8) * 2);
         }
-        if (!cut) {
+        bool odd = false;                          // an infinity or NaN in a tile that some row does not see all of
+        if (cut) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t w0 = (&vv[0].x)[k], w1 = (&vv[1].x)[k], w2 = (&vv[2].x)[k], w3 = (&vv[3].x)[k];
-            const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-            const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+          for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-              mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
-            }
+            for (int k = 0; k < 4; ++k) odd |= (&vv[r].x)[k] != finite_bf16x2((&vv[r].x)[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w0 = (&vv[0].x)[k], w1 = (&vv[1].x)[k], w2 = (&vv[2].x)[k], w3 = (&vv[3].x)[k];
+          if (cut) w0 = finite_bf16x2(w0), w1 = finite_bf16x2(w1), w2 = finite_bf16x2(w2), w3 = finite_bf16x2(w3);
+          const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+          const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+            mma16816<true>(O[4 * v8 + k][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
           }
-        } else {
-          // tokens that some rows do not see: added token by token, so that infinities and NaN of a hidden
-          // token reach no row (a product would multiply them by its zero numerator)
+        }
+        if (__any_sync(0xFFFFFFFFu, odd)) {
+          // infinities and NaN are added token by token to the rows that see them (the product would multiply a
+          // hidden token's by its zero numerator and make every row NaN)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             for (int tt = 0; tt < 4; ++tt) {
@@ -989,8 +1003,9 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
                   if (tk < cnt && pos0 + tk < lim[n][c]) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                      O[4 * v8 + k][n][c] = fmaf(pr, bf16lo(wd[k]), O[4 * v8 + k][n][c]);
-                      O[4 * v8 + k][n][c + 2] = fmaf(pr, bf16hi(wd[k]), O[4 * v8 + k][n][c + 2]);
+                      const uint32_t f = finite_bf16x2(wd[k]);
+                      if ((wd[k] ^ f) & 0xFFFFu) O[4 * v8 + k][n][c] += pr * bf16lo(wd[k]);
+                      if ((wd[k] ^ f) >> 16) O[4 * v8 + k][n][c + 2] += pr * bf16hi(wd[k]);
                     }
                   }
                 }
