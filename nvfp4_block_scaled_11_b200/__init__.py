@@ -799,8 +799,31 @@ def _extent(t: torch.Tensor) -> tuple[int, int]:
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors may share elements.  Views of one buffer with the same strides (q, k and v side by side in
+    a row) are told apart exactly; others by the bytes that they span."""
     (a0, a1), (b0, b1) = _extent(a), _extent(b)
-    return a0 < b1 and b0 < a1
+    if not (a0 < b1 and b0 < a1):
+        return False
+    sizes = list(zip(a.shape, a.stride(), b.shape, b.stride()))
+    e = a.element_size()
+    off = b.data_ptr() - a.data_ptr()
+    if e != b.element_size() or off % e or any(na > 1 and nb > 1 and sa != sb for na, sa, nb, sb in sizes):
+        return True
+    # b's element j is a's element i where sum (i_d - j_d) stride_d is the distance of their first ones
+    dims = sorted(((sa if na > 1 else sb, 1 - nb, na - 1) for na, sa, nb, sb in sizes if (na > 1 or nb > 1) and (sa if na > 1 else sb)),
+                  reverse=True)
+    reach = [(0, 0)]
+    for s, lo, hi in reversed(dims):
+        reach.append((reach[-1][0] + lo * s, reach[-1][1] + hi * s))
+    reach.reverse()
+
+    def hits(d: int, left: int) -> bool:
+        if d == len(dims):
+            return left == 0
+        s, lo, hi = dims[d]
+        r_lo, r_hi = reach[d + 1]
+        return any(hits(d + 1, left - i * s) for i in range(max(lo, -(-(left - r_hi) // s)), min(hi, (left - r_lo) // s) + 1))
+    return hits(0, off // e)
 
 
 class _KvStore(ctypes.Structure):
@@ -898,6 +921,8 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
     if k.geometry != v.geometry:
         raise ValueError("k and v stores disagree on their sizes or device")
     B, Hq, Tq, D = q.shape
+    if D not in (64, 128, 256):
+        raise ValueError("head_dim must be 64, 128 or 256")
     dev = q.device
     if D != k.D or dev != k.device:
         raise ValueError("q and the stores disagree on head_dim or device")
@@ -923,6 +948,8 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
         d.lens = lens.data_ptr()
         hint = most if max_mid is None else min(max(int(max_mid), 0), most)
     else:
+        if any(n < 0 or n >> 31 for n in lens):
+            raise ValueError("lengths are 32-bit and not negative")
         d.n_sink, d.n_mid, d.head, d.n_window = lens
         hint = int(lens[1])
     if slots is not None:
@@ -1079,9 +1106,10 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
             if o.shape != s or o.dtype != dtype or o.device != dev:
                 raise ValueError("out must have x's shape, dtype and device")
             _no_shared_elements(o, "out")
-            if any(o.data_ptr() == outs[i].data_ptr() and o.numel() for i in range(j)):
-                raise ValueError("two outputs are the same tensor")
-            if not (o.data_ptr() == a.data_ptr() and o.stride() == sx) and any(_overlap(o, b) for b in xs):
+            if any(_overlap(o, outs[i]) for i in range(j)):
+                raise ValueError("two outputs share elements")
+            same = o.data_ptr() == a.data_ptr() and o.stride() == sx
+            if any(_overlap(o, b) for i, b in enumerate(xs) if not (same and i == j)):
                 raise ValueError("out must be x itself or not overlap any x")
         so = o.stride()
         d = descs[j]

@@ -192,7 +192,8 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* wo
   p.ws_meta = static_cast<int4*>(workspace);
   p.ws_o = reinterpret_cast<float*>(p.ws_meta + splits);
   p.ws_ml = reinterpret_cast<float2*>(p.ws_o + ws_rows * d.D);
-  // sequences that are all alike and parts that hold whole jobs: no cut inside a job
+  // sequences that are all alike and parts that hold whole jobs: no cut inside a job (a job is enough for a part)
+  static_assert(kKaJobUnits + 1 >= kKaMinUnits, "jobs of the least work must not be cut");
   const bool join = splits > 1 && !(d.lens == nullptr && d.slot == nullptr && jobs % splits == 0);
   const bool bf = d.dtype == NVFP4_BF16;
   cudaStream_t s = S(stream);

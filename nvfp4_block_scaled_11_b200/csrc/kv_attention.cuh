@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
 #pragma unroll
       for (int o = BPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
       int e = (int)(__float_as_uint(mx) >> 23) - 127;                  // floor(log2), exact for normal values
-      e = mx > 0.0f && mx <= FLT_MAX ? max(-100, min(100, e)) : 0;
+      e = mx > 0.0f && mx <= FLT_MAX ? max(-126, min(126, e)) : 0;    // 2^e and 2^-e are normal
       const float down = sign * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

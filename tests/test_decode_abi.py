@@ -1,6 +1,7 @@
 """Argument validation of the decode entry points (attention over the cache, rotary positions, page copies), all decided
 on the host before any CUDA work (fake device pointers, no GPU needed), and the host-side sizes."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -191,3 +192,21 @@ def test_parts_of_the_work_cover_it():
                 assert p.of(starts[j] + costs[j] - 1) - cut + 2 == len(got)
             for c, _, _ in got[2:]:
                 assert p.start(c - 1) > starts[j] + J      # no later cut claims to be the first
+
+
+def test_shared_elements_of_views_are_found_exactly():
+    """Views of one buffer with the same strides against the sets of their elements."""
+    rnd = random.Random(3)
+    base = torch.arange(4 * 6 * 10 * 8).view(4, 6, 10, 8)
+    seen = set()
+    for _ in range(400):
+        def view():
+            s = [slice(a := rnd.randrange(n), rnd.randrange(a, n) + 1) for n in base.shape]
+            return base[tuple(s)]
+        a, b = view(), view()
+        share = bool(set(a.flatten().tolist()) & set(b.flatten().tolist()))
+        assert nv._overlap(a, b) == share and nv._overlap(b, a) == share
+        seen.add(share)
+    assert seen == {True, False}
+    t = base.transpose(1, 2)
+    assert nv._overlap(base[:, :2], t[:, :2]) and not nv._overlap(base[:2], t[2:])   # other strides: by their span

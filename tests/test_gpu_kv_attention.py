@@ -327,3 +327,28 @@ def test_refusals():
         nv.KvStore(k.sink.cuda(), k.window.cuda(), k.codes.cuda(), k.scales[:3].cuda(), k.gscale.cuda())
     assert nv.kv_attention(q[:0], s, s, lens).shape == (0, 4, 1, 128)
     assert nv.kv_attention(q[:, :, :0], s, s, lens).shape == (2, 4, 0, 128)
+
+
+@pytest.mark.parametrize("p", [-112, 60, 112])
+@pytest.mark.parametrize("D", [64, 256])
+def test_far_ranges_of_query_and_keys_cancel(p, D):
+    """q times 2^p against keys times 2^-p: every product is the same, so is every bit."""
+    gen = torch.Generator().manual_seed(D)
+    q = _q(gen, 2, 4, 1, D, BF).cuda()
+    lens = torch.tensor([(16, 301, 16, 29), (16, 33, 0, 16)], dtype=torch.int32).cuda()
+    k, v = (kvref.Side(gen, 2, 1, D, 16, 32, 2, 333) for _ in (0, 1))
+    want = nv.kv_attention(q, k.store(nv), v.store(nv), lens, want_lse=True)
+    k.sink, k.window, k.gscale = (t * 2.0 ** -p for t in (k.sink, k.window, k.gscale))
+    got = nv.kv_attention(q * 2.0 ** p, k.store(nv), v.store(nv), lens, want_lse=True)
+    assert torch.isfinite(got[0]).all() and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals_of_sizes_in_words():
+    gen = torch.Generator().manual_seed(0)
+    k = kvref.Side(gen, 1, 1, 80, 0, 16, 1, 16).store(nv)
+    with pytest.raises(ValueError, match="head_dim"):
+        nv.kv_attention(torch.zeros(1, 1, 1, 80, dtype=BF, device="cuda"), k, k, (0, 16, 0, 16))
+    k = kvref.Side(gen, 1, 1, 64, 0, 16, 1, 16).store(nv)
+    for lens in ((0, 2 ** 32 + 5, 0, 1), (0, -1, 0, 1), (0, 5, 2 ** 31, 1)):
+        with pytest.raises(ValueError, match="lengths"):
+            nv.kv_attention(torch.zeros(1, 1, 1, 64, dtype=BF, device="cuda"), k, k, lens)

@@ -170,3 +170,20 @@ def test_refusals():
         nv.rope_frequencies(8, scaling=dict(type="other", factor=2))
     with pytest.raises(ValueError):
         nv.rope_frequencies(8, scaling=dict(type="yarn", factor=2))
+
+
+def test_outputs_beside_their_inputs_and_shared_ones():
+    """Rows of one buffer that lie side by side are told apart; a tensor written while another reads it is refused."""
+    f, _ = nv.rope_frequencies(16)
+    pos = torch.arange(8, device="cuda")
+    buf = torch.randn(2, 8, 3 * 4 * 16, device="cuda").view(2, 8, 12, 16).transpose(1, 2)
+    q, k, o = buf[:, :4], buf[:, 4:8], buf[:, 8:]
+    want = nv.rope([q.clone(), k.clone()], pos, f)
+    nv.rope(q, pos, f, out=o)
+    assert torch.equal(o, want[0])
+    nv.rope([q, k], pos, f, out=[q, k])
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    new = torch.empty(2, 4, 8, 16, device="cuda")
+    for xs, outs in (([q, q], [q, new]), ([q, buf[:, 3:7]], [q, new]), ([q, k], [o, buf[:, 7:11]]), ([q, k], [new, new])):
+        with pytest.raises(ValueError):
+            nv.rope(xs, pos, f, out=outs)
