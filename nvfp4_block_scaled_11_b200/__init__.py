@@ -14,6 +14,7 @@ import ctypes
 import math
 import numbers
 import os
+import struct
 
 import torch
 
@@ -843,6 +844,11 @@ class _KvAttentionDesc(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+# The same record packed in one go (setting its fields one by one takes 2.5 us of a call's 15).
+_KV_ATTENTION = struct.Struct("@3Q11q%ds%ds6q3Q6if0q" % (2 * (ctypes.sizeof(_KvStore),)))
+assert _KV_ATTENTION.size == ctypes.sizeof(_KvAttentionDesc)
+
+
 class KvStore:
     """One side (K or V) of a mixed-precision cache as kv_attention reads it, checked once: sink [slots, H, s, D]
     and window [slots, H, w, D] (BF16; zero rows if there are none), codes uint8 [pages, H, rows, D/2], scales
@@ -873,8 +879,8 @@ class KvStore:
         self.sink_rows, self.window_rows, self.device = sink.shape[2], window.shape[2], codes.device
         self.geometry = (S, H, D, pages, rows, self.sink_rows, self.window_rows, codes.device)
         self._keep = (sink, window, codes, scales, gscale)
-        self._desc = _KvStore(*(t.data_ptr() for t in self._keep), 1 if gscale.numel() > 1 else 0, int(bool(rotate)),
-                              int(bool(tile_layout)))
+        self._desc = bytes(_KvStore(*(t.data_ptr() for t in self._keep), 1 if gscale.numel() > 1 else 0, int(bool(rotate)),
+                                    int(bool(tile_layout))))
 
 
 _kv_splits_memo: dict = {}
@@ -929,15 +935,14 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
     if k.H == 0 or Hq % k.H:
         raise ValueError("query heads must be a multiple of the K/V heads")
     rows = Hq // k.H * Tq
-    d = _KvAttentionDesc()
-    most = k.page_rows
+    most, cols, table_at, lens_at, slots_at, ends = k.page_rows, 0, 0, 0, 0, (0, 0, 0, 0)
     if table is not None:
         _cuda(table, "table")
         if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != k.slots or table.device != dev:
             raise ValueError("table must be int32 [slots, cols] on q's device")
-        d.table, d.table_cols = table.data_ptr(), table.shape[1]
-        most *= table.shape[1]
-        if table.shape[1] == 0:
+        table_at, cols = table.data_ptr(), table.shape[1]
+        most *= cols
+        if cols == 0:
             raise ValueError("table has no columns")
     elif k.pages < k.slots:
         raise ValueError("without a table every slot needs its own page")
@@ -945,22 +950,21 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
         _cuda(lens, "lens")
         if lens.dtype != torch.int32 or lens.shape != (k.slots, 4) or lens.device != dev:
             raise ValueError("lens must be int32 [slots, 4] on q's device")
-        d.lens = lens.data_ptr()
+        lens_at = lens.data_ptr()
         hint = most if max_mid is None else min(max(int(max_mid), 0), most)
     else:
-        if any(n < 0 or n >> 31 for n in lens):
+        _, hint, _, _ = ends = tuple(lens)
+        if min(ends) < 0 or max(ends) >> 31:
             raise ValueError("lengths are 32-bit and not negative")
-        d.n_sink, d.n_mid, d.head, d.n_window = lens
-        hint = int(lens[1])
     if slots is not None:
         _cuda(slots, "slots")
         if slots.dtype != torch.int32 or slots.shape != (B,) or slots.device != dev:
             raise ValueError("slots must be int32 [B] on q's device")
-        d.slot = slots.data_ptr()
+        slots_at = slots.data_ptr()
     elif B > k.slots:
         raise ValueError("more batch rows than slots")
     if out is None:
-        out = torch.empty((B, Hq, Tq, D), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _rows(out, "out")
         if out.shape != q.shape or out.dtype != q.dtype or out.device != dev:
@@ -973,7 +977,7 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
         if lse.device != dev:
             raise ValueError("lse must be on q's device")
     elif want_lse:
-        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, Hq, Tq), dtype=torch.float32)
     if splits is None:
         splits, need = _kv_splits(dev, B, k.H, rows, D, max(hint, 0))
     else:
@@ -986,16 +990,13 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
         _cuda(workspace, "workspace")
         if workspace.device != dev or workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace must hold {need} bytes on q's device")
-    d.q, d.out = q.data_ptr(), out.data_ptr()
-    if lse is not None:
-        d.lse = lse.data_ptr()
-    d.q_sb, d.q_sh, d.q_st = q.stride()[:3]
-    d.out_sb, d.out_sh, d.out_st = out.stride()[:3]
-    d.B, d.Hq, d.Hkv, d.Tq, d.D = B, Hq, k.H, Tq, D
-    d.k, d.v = k._desc, v._desc
-    d.slots, d.sink_rows, d.window_rows, d.pages, d.page_rows = k.slots, k.sink_rows, k.window_rows, k.pages, k.page_rows
-    d.dtype, d.causal, d.scale = DTYPE_CODE[q.dtype], int(bool(causal)), D ** -0.5 if scale is None else scale
-    _launch(dev, lib().nvfp4_kv_attention, ctypes.byref(d), splits, None if workspace is None else workspace.data_ptr(),
+    q_sb, q_sh, q_st, _ = q.stride()
+    o_sb, o_sh, o_st, _ = out.stride()
+    desc = _KV_ATTENTION.pack(
+        q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), q_sb, q_sh, q_st, o_sb, o_sh, o_st, B, Hq, k.H, Tq, D,
+        k._desc, v._desc, k.slots, k.sink_rows, k.window_rows, k.pages, k.page_rows, cols, slots_at, table_at, lens_at, *ends,
+        DTYPE_CODE[q.dtype], 1 if causal else 0, D ** -0.5 if scale is None else scale)
+    _launch(dev, lib().nvfp4_kv_attention, desc, splits, None if workspace is None else workspace.data_ptr(),
             need if workspace is not None else 0)
     return (out, lse) if want_lse else out
 
@@ -1051,6 +1052,8 @@ class _RopeTensor(ctypes.Structure):
     _fields_ = [("x", _P), ("out", _P), *((n, _I64) for n in ("heads", "x_sb", "x_sh", "x_st", "out_sb", "out_sh", "out_st"))]
 
 
+_ROPE_TENSOR = struct.Struct("@2Q7q")     # the same, packed in one go
+assert _ROPE_TENSOR.size == ctypes.sizeof(_RopeTensor)
 ROPE_MAX = 8
 
 
@@ -1089,7 +1092,7 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
     pos_shape, ps = positions.shape, positions.stride()
     if pos_shape not in ((T,), (B, T)) or positions.device != dev:
         raise ValueError("positions must be [T] or [B, T] on x's device")
-    descs = (_RopeTensor * len(xs))()
+    descs = []
     for j, a in enumerate(xs):
         if j:
             _rows(a, "x")
@@ -1100,7 +1103,7 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
             s = s0
         sx = a.stride()
         if not given:
-            o = outs[j] = torch.empty(s, dtype=dtype, device=dev)
+            o = outs[j] = torch.empty_like(a, memory_format=torch.contiguous_format)
         else:
             o = _rows(outs[j], "out")
             if o.shape != s or o.dtype != dtype or o.device != dev:
@@ -1111,16 +1114,9 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
             same = o.data_ptr() == a.data_ptr() and o.stride() == sx
             if any(_overlap(o, b) for i, b in enumerate(xs) if not (same and i == j)):
                 raise ValueError("out must be x itself or not overlap any x")
-        so = o.stride()
-        d = descs[j]
-        d.x, d.out, d.heads = a.data_ptr(), o.data_ptr(), s[-3]
-        if nd == 4:
-            d.x_sb, d.x_sh, d.x_st, _ = sx
-            d.out_sb, d.out_sh, d.out_st, _ = so
-        else:
-            d.x_sh, d.x_st, _ = sx
-            d.out_sh, d.out_st, _ = so
-    _launch(dev, lib().nvfp4_rope, descs, len(xs), B, T, D, rot, 1 if interleaved else 0, dt, positions.data_ptr(),
+        x_st, o_st = (sx, o.stride()) if nd == 4 else ((0, *sx), (0, *o.stride()))
+        descs.append(_ROPE_TENSOR.pack(a.data_ptr(), o.data_ptr(), s[-3], *x_st[:3], *o_st[:3]))
+    _launch(dev, lib().nvfp4_rope, b"".join(descs), len(xs), B, T, D, rot, 1 if interleaved else 0, dt, positions.data_ptr(),
             1 if positions.dtype == torch.int64 else 0, ps[0] if len(ps) == 2 else 0, ps[-1], freqs.data_ptr(), mscale,
             1 if inverse else 0)
     return outs[0] if one else outs
