@@ -66,7 +66,8 @@ int launch_kv_attention_d(const KvAttnParams& p, bool bf, int nt, unsigned parts
 }
 
 // Query rows of a CTA in units of 8: one K/V head's rows fit 8 for most decode steps; more rows share the
-// expansion of the codes in tiles of 16.
+// expansion of the codes in tiles of 16.  16 sequences of 8192 tokens, 2 K/V heads, 16 rows, tiles of 16 against 8 (us):
+// D = 64 21.1 / 22.1, D = 128 26.0 / 28.2, D = 256 42.0 / 45.0; 64 rows, D = 128: 69.1 / 82.0.
 int ka_row_units(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 // CTAs of the attention kernel that an SM holds (its launch bounds and shared memory).
@@ -251,10 +252,14 @@ int nvfp4_rope(const nvfp4_rope_tensor* tensors, int count, int64_t B, int64_t T
   const int64_t half = rot / 2, pieces = (interleaved ? rot : half) / v + (D - rot) / v;
   const int64_t per_pass = std::max<int64_t>(1, kRopeThreads / std::max<int64_t>(1, pieces));
   const int sms = sm_count();
-  // tokens per CTA (of one sequence): as many as leave two CTAs per SM, up to 32 passes of its threads over (token, head) rows
-  int64_t tile = 1;
-  while (tile < 32 && 2 * tile * half <= kRopeSmemPairs && tile < T && B * T / (2 * tile) >= 2 * sms && 2 * tile * heads <= 32 * per_pass)
-    tile *= 2;
+  // Tokens per CTA (of one sequence): as few as make one wave of CTAs, or two or more waves where its angles would pass
+  // the shared memory.  A wave that is not full costs as much as a full one; 8192 tokens of 40 heads with tiles
+  // of 8 (1.4 waves) / 10 / 12 (0.9) / 16 / 24: 34.8 / 37.8 / 31.4 / 33.6 / 39.4 us, 2 x 2047 tokens of 32 heads of 64 FP32
+  // channels with 4 / 6 (0.9) / 8 / 12: 16.8 / 15.0 / 16.0 / 18.7 us.
+  const int64_t most = std::min<int64_t>(std::max<int64_t>(T, 1), std::min<int64_t>(32, half ? kRopeSmemPairs / half : 32));
+  const int64_t wave = (int64_t)sms * kRopeCtasPerSm, waves = (B * T + wave * most - 1) / (wave * most);
+  int64_t tile = std::max<int64_t>(1, (B * T + wave * waves - 1) / (wave * waves));
+  while (tile < most && B * ((T + tile - 1) / tile) > wave * waves) ++tile;    // sequences end in short tiles
   p.tile = (int)tile;
   p.tiles = (int)((T + tile - 1) / tile);
   const int64_t gx = B * p.tiles;
