@@ -9,23 +9,38 @@
 // In the middle k_t = H16/4 (code e4m3 g_k), so q . k_t = (H16/4 q) . (code e4m3) g_k: the query is rotated
 // once and the keys never; O's middle part is accumulated in rotated space and turned back once.
 //
-// One pass over the tokens with a running maximum and sum (kv_attn_kernel), a CTA per (sequence, K/V head,
-// tile of query rows, range of the middle); ranges are joined by kv_attn_combine_kernel.  The bytes of
-// the cache bound it (2 (D/2 + D/16) per token and K/V head), so the design keeps copies in flight and the
-// instructions per byte low:
+// One pass over the tokens with a running maximum and sum (kv_attn_kernel); what a CTA did not finish of a
+// job (sequence, K/V head, tile of query rows) is joined by kv_attn_combine_kernel.  Bytes to move: 2 (D/2 + D/16) per
+// middle token and K/V head, which at the copy rate of a B200 (6549 GB/s) is 92.5 us for 16 sequences of
+// 32768 tokens, 8 K/V heads, D = 128; the kernel takes 140 us there, 4.3 TB/s.  It is not the bytes that bound it but
+// turning 4-bit codes into operands: per tile of 32 tokens a warp issues 623 instructions, of them 128 converts
+// (e2m1x2) and 128 multiplies (f16x2) that hold their pipe two cycles each and were measured not to overlap
+// (15.5 cycles per 4 + 4), and 48 products.  Counters at that size: 2.3 instructions per cycle and SM,
+// converts' pipe 43 %, FP16 23 %, tensor pipe 35 %, DRAM 51 %; of a warp's 2815 cycles per tile 20 wait for
+// copies, 820 issue them and 1880 compute.  The design keeps copies in flight and instructions per byte low:
 // * every warp owns its tiles of 32 tokens and its own ring of shared-memory stages filled by cp.async: no
-//   CTA-wide barrier inside the loop, rows behind the end arrive as zeros;
+//   CTA-wide barrier inside the loop, rows behind the end arrive as zeros.  Bulk copies take the same bytes with
+//   one instruction per row group, but each lane's copy is issued by itself (78 cycles): 157 us issued by every
+//   warp, 147 by a fifth warp for all four;
 // * code * e4m3 has at most 6 significant bits and lies in [2^-10, 2688], so the products' operands are exact
 //   in FP16: one convert and one multiply give two elements, and m16n8k16 products with FP32 accumulators
-//   take keys (or values' channels) as the 16 rows and query rows as the 8 columns.  tcgen05 would want
-//   128 rows of expanded tiles in shared memory for 8 useful columns: the expansion would cross shared
-//   memory once more and the accumulators TMEM, for a product that is not what bounds the pass;
+//   take keys (or values' channels) as the 16 rows and query rows as the 8 columns.  A decode step has 1 to 16
+//   query rows per K/V head: tcgen05 would spend a 128-row tile on them.  Keys can go to it as stored (block-scaled
+//   FP4, the query as 8 FP4 terms of 16 columns each); built and measured, it took 180 us where this takes
+//   140, since 128-token operands need their copies, fences and TMEM reads in step and the values still have to be
+//   expanded;
 // * the rotated query is split into two FP16 terms (22 bits after a power-of-two row scale), so scores
 //   keep FP32 accuracy; the numerators are rounded to FP16 once, scaled by 2^10 (2^-12 relative error
 //   each down to 2^-24 of the row's maximum; sums are taken in FP32 before that rounding);
 // * S^T = K Q^T leaves (token, query) fragments; movmatrix turns the FP16 numerators into the second
 //   product's operand; V is packed along channels, so pairs of tokens are interleaved nibble by nibble
-//   (two logic operations per 8 codes and token) before the converts.
+//   (two logic operations per 8 codes and token) before the converts;
+// * the reference that numerators are taken against follows the maximum only when a score passes it by 2^5, so almost
+//   no tile rescales the accumulators;
+// * one job per CTA leaves SMs idle when sequences differ in length: all tokens of the call are cut evenly instead
+//   (see ka_units).  One sequence of 32768 tokens: 20.6 us; 48 of up to 8191: 46.8; 8 draft steps of 4 tokens,
+//   D = 64: 15.4; D = 256 with 16 query heads on one K/V head: 38.0; 301 tokens: 8.3 (of which launch, the query's
+//   rotation and three dependent rounds of loads are most).
 #pragma once
 
 #include <float.h>
@@ -40,7 +55,10 @@ namespace nvfp4 {
 
 constexpr int kKaWarps = 4;            // warps per CTA, each with its own tiles
 constexpr int kKaTile = 32;            // middle tokens per tile
-constexpr int kKaJobUnits = 3;         // what starting and ending a job costs, in units of work (4 tiles)
+// What starting and ending a job costs, in units of work (4 tiles).  Measured with 1 / 2 / 3 / 5 / 8 (us): 48 ragged sequences
+// 52.4 / 51.6 / 49.2 / 52.8 / 57.1, draft tokens 23.3 / 20.1 / 17.6 / 18.3 / 19.5, 16 sequences with D = 256 42.1 / 41.0 /
+// 36.9 / 35.9 / 38.1.
+constexpr int kKaJobUnits = 3;
 constexpr int kKaMinUnits = 4;         // least units per part: shorter ones cost more in joining than they win
 constexpr int kKaMaxSplits = 65535;
 constexpr int kKaJoinWarps = 8;        // warps that join the pieces of one query row
@@ -83,6 +101,7 @@ struct KaShape {
   static constexpr int kCodeRow = D / 2, kScaleRow = D / 16;
   static constexpr int kKC = 0, kVC = kKaTile * kCodeRow, kKS = 2 * kKaTile * kCodeRow, kVS = kKS + kKaTile * kScaleRow;
   static constexpr int kStageBytes = 2 * kKaTile * (kCodeRow + kScaleRow);
+  // (three stages at D = 128 gain nothing: the copies are never waited for)
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kRing = kKaWarps * kStages * kStageBytes;
 };
@@ -268,6 +287,8 @@ __device__ __forceinline__ void ka_store(char* out, int64_t i, float x) {
 }
 
 // D: head_dim; NT: query rows / 8 of a CTA; QBF: q and out are BF16 (else FP16).
+// CTAs per SM: as many as registers allow without spills in the loop.  D = 128, NT = 1 with 3 (146 registers) against
+// 4 (128 registers, spills): one long sequence 21.0 / 24.0 us, ragged 46.7 / 49.2, large 144.9 / 148.0.
 template <int D, int NT, bool QBF>
 __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3))
     kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
@@ -642,33 +663,37 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
       // ---- S^T = K Q^T: rows are tokens (two tiles of 16), columns query rows ----
       float S[2][NT][4];
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int cc = 0; cc < KCH; ++cc) {
+        uint32_t kw[2][2][KW], ks[2][2][KW / 2];   // [token tile][rows perm and perm + 8]; scales doubled into both halves
 #pragma unroll
-        for (int cc = 0; cc < KCH; ++cc) {
-          uint32_t kw[2][KW], ks[2][KW / 2];     // rows perm and perm + 8; scales doubled into both halves
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int row = 8 * k + 16 * a;      // + perm, in the lane's offsets
+            const int row = 8 * k + 16 * a;        // + perm, in the lane's offsets
             if constexpr (KW == 4) {
               const uint4 v = *reinterpret_cast<const uint4*>(st + (cc ? k_read2 : k_read) + row * Sh::kCodeRow);
-              kw[k][0] = v.x, kw[k][1] = v.y, kw[k][2] = v.z, kw[k][3] = v.w;
+              kw[a][k][0] = v.x, kw[a][k][1] = v.y, kw[a][k][2] = v.z, kw[a][k][3] = v.w;
               const uint32_t h = e4m3x2_f16x2(*reinterpret_cast<const unsigned short*>(st + ks_read + row * Sh::kScaleRow + 8 * cc));
-              ks[k][0] = both_lo(h);
-              ks[k][1] = both_hi(h);
+              ks[a][k][0] = both_lo(h);
+              ks[a][k][1] = both_hi(h);
             } else {
               const uint2 v = *reinterpret_cast<const uint2*>(st + k_read + row * Sh::kCodeRow);
-              kw[k][0] = v.x, kw[k][1] = v.y;
-              ks[k][0] = both_lo(e4m3x2_f16x2(st[ks_read + row * Sh::kScaleRow]));
+              kw[a][k][0] = v.x, kw[a][k][1] = v.y;
+              ks[a][k][0] = both_lo(e4m3x2_f16x2(st[ks_read + row * Sh::kScaleRow]));
             }
           }
+        // a word of 8 codes feeds two steps; both token tiles take the query's fragments while they are in registers
+        // (tile after tile: D = 256 38.6 against 38.0 us, ragged D = 128 47.2 against 46.8)
 #pragma unroll
-          for (int wd = 0; wd < KW; ++wd) {      // a word of 8 codes feeds two steps
+        for (int wd = 0; wd < KW; ++wd)
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
             uint32_t h[2][4];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              e2m1x8(kw[k][wd], h[k]);
+              e2m1x8(kw[a][k][wd], h[k]);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) h[k][c] = hmul2(h[k][c], ks[k][wd >> 1]);
+              for (int c = 0; c < 4; ++c) h[k][c] = hmul2(h[k][c], ks[a][k][wd >> 1]);
             }
 #pragma unroll
             for (int j2 = 0; j2 < 2; ++j2) {
@@ -682,7 +707,7 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
               }
             }
           }
-        }
+      }
       // ---- numerators (fac >= 0: maxima are taken before it is applied) ----
       float mx[NT][2];
 #pragma unroll
