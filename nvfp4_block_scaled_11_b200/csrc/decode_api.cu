@@ -35,7 +35,7 @@ int raise_smem(int bytes) {
 }
 
 template <int D, int NT, bool QBF>
-int launch_kv_attention(const KvAttnParams& p, unsigned parts, bool join, cudaStream_t s) {
+int launch_kv_attention(const KvAttnParams& p, unsigned parts, unsigned join, cudaStream_t s) {
   constexpr int smem = KaSmem<D, NT, QBF>::kBytes;
   if (int rc = raise_smem<kv_attn_kernel<D, NT, QBF>>(smem)) return rc;
   kv_attn_kernel<D, NT, QBF><<<parts, kKaWarps * 32, smem, s>>>(p);
@@ -46,7 +46,7 @@ int launch_kv_attention(const KvAttnParams& p, unsigned parts, bool join, cudaSt
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(parts, 8 * NT);
+    cfg.gridDim = dim3(join, std::min(p.R, 8 * NT));
     cfg.blockDim = dim3(kKaJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = &at;
@@ -60,7 +60,7 @@ int launch_kv_attention(const KvAttnParams& p, unsigned parts, bool join, cudaSt
 }
 
 template <int D>
-int launch_kv_attention_d(const KvAttnParams& p, bool bf, int nt, unsigned parts, bool join, cudaStream_t s) {
+int launch_kv_attention_d(const KvAttnParams& p, bool bf, int nt, unsigned parts, unsigned join, cudaStream_t s) {
   if (nt == 1) return bf ? launch_kv_attention<D, 1, true>(p, parts, join, s) : launch_kv_attention<D, 1, false>(p, parts, join, s);
   return bf ? launch_kv_attention<D, 2, true>(p, parts, join, s) : launch_kv_attention<D, 2, false>(p, parts, join, s);
 }
@@ -195,7 +195,9 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* wo
   p.ws_ml = reinterpret_cast<float2*>(p.ws_o + ws_rows * d.D);
   // sequences that are all alike and parts that hold whole jobs: no cut inside a job (a job is enough for a part)
   static_assert(kKaJobUnits + 1 >= kKaMinUnits, "jobs of the least work must not be cut");
-  const bool join = splits > 1 && !(d.lens == nullptr && d.slot == nullptr && jobs % splits == 0);
+  const bool cuts = splits > 1 && !(d.lens == nullptr && d.slot == nullptr && jobs % splits == 0);
+  p.by_job = jobs <= splits;
+  const unsigned join = !cuts ? 0 : p.by_job ? (unsigned)jobs : (unsigned)splits;   // entries of ws_meta
   const bool bf = d.dtype == NVFP4_BF16;
   cudaStream_t s = S(stream);
   if (d.D == 64) return launch_kv_attention_d<64>(p, bf, nt, (unsigned)splits, join, s);

@@ -38,8 +38,8 @@
 // * the reference that numerators are taken against follows the maximum only when a score passes it by 2^5, so almost
 //   no tile rescales the accumulators;
 // * one job per CTA leaves SMs idle when sequences differ in length: all tokens of the call are cut evenly instead
-//   (see ka_units).  One sequence of 32768 tokens: 20.6 us; 48 of up to 8191: 46.8; 8 draft steps of 4 tokens,
-//   D = 64: 15.4; D = 256 with 16 query heads on one K/V head: 38.0; 301 tokens: 8.3 (of which launch, the query's
+//   (see ka_units).  One sequence of 32768 tokens: 19.9 us; 48 of up to 8191: 47.2; 8 draft steps of 4 tokens,
+//   D = 64: 13.7; D = 256 with 16 query heads on one K/V head: 35.7; 301 tokens: 8.4 (of which launch, the query's
 //   rotation and three dependent rounds of loads are most).
 #pragma once
 
@@ -93,7 +93,8 @@ struct KvAttnParams {
   float scale_log2;        // scale * log2(e)
   float* ws_o;             // [parts, 2, rows, D] sums of the jobs that a part shares with the part before / after it
   float2* ws_ml;           // [parts, 2, rows] their references (base 2) and denominators
-  int4* ws_meta;           // [parts] the job that a part's start cuts first: sequence, head and row tile, parts, flag
+  int4* ws_meta;           // jobs that are cut: sequence, head and row tile, first part, last part (-1: not cut)
+  int by_job;              // ws_meta is indexed by the job (no more of them than parts); else by the part that begins it
 };
 
 template <int D>
@@ -310,7 +311,6 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
   __shared__ int64_t scan[kKaWarps + 1];
   __shared__ int found_b;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
   const int part = blockIdx.x, jobs_per_seq = p.Hkv * p.row_tiles;
 
@@ -360,20 +360,12 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
     b = found_b;
   }
   const KaParts parts(total, gridDim.x);
-  if (part >= parts.n) {
-    if (gridDim.x > 1 && tid == 0) p.ws_meta[part] = make_int4(0, 0, 0, 0);
-    return;
-  }
+  if (gridDim.x > 1 && tid == kKaWarps * 32 - 1 && !p.by_job) p.ws_meta[part].w = -1;
+  if (part >= parts.n) return;
   int64_t u = parts.start(part);
   const int64_t u_end = parts.start(part + 1);
   KaSeq sq = ka_sequence(p, b);
   int cost = ka_units(sq);
-  if (gridDim.x > 1 && tid == 0) {
-    const int64_t in_seq = u - seq_start, job = in_seq / cost, s = seq_start + job * cost + kKaJobUnits;
-    const bool first = s < u && parts.start(part - 1) <= s;           // the first cut inside its job joins it
-    p.ws_meta[part] = first ? make_int4(b, (int)job, parts.of(s - kKaJobUnits + cost - 1) - part + 2, 1) : make_int4(0, 0, 0, 0);
-  }
-
   while (u < u_end) {
     if (u - seq_start >= (int64_t)cost * jobs_per_seq) {
       seq_start += (int64_t)cost * jobs_per_seq;
@@ -583,6 +575,12 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
         // positions this row sees: all before the limit (rows past R restrict nothing and are not written)
         limit[row] = p.causal && r < p.R ? max(sq.len - p.Tq + r / p.G + 1, 0) : sq.len;
       }
+    }
+    if (gridDim.x > 1 && tid == kKaWarps * 32 - 1) {   // (the last warps have no query row of most calls)
+      int4* e = p.ws_meta + (p.by_job ? (int64_t)b * jobs_per_seq + job : part);
+      const bool begun = first_unit == 0, done = last_unit == units;
+      if (begun && !done) *reinterpret_cast<int2*>(e) = make_int2(b, job), e->z = part;
+      if (p.by_job ? done : begun && !done) e->w = p.by_job ? (begun ? -1 : part) : parts.of(u - 1);
     }
     __syncthreads();
 
@@ -1041,6 +1039,9 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
     }
 
     // ---- join the warps ----
+    // The joining kernel may be launched from here on: earlier, its waiting CTAs fill the SMs that have room first and
+    // stay together there (one long sequence 21.9 against 19.9 us).
+    if (u >= u_end) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1099,22 +1100,24 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
   }
 }
 
-// Joins the jobs that cuts fall into: the CTAs of the first cut of each, one per query row.
+// Joins the jobs that cuts fall into, a CTA per entry of ws_meta and query row.  Entries per part alone would launch
+// thousands of CTAs that find nothing to do: draft tokens 15.3 against 13.7 us, D = 256 38.0 / 35.7, one long sequence
+// 20.8 / 19.9; 48 ragged sequences, where nearly every part begins a job that is cut, 46.3 / 47.2.
 template <int D, int NT, bool QBF>
 __global__ void __launch_bounds__(kKaJoinWarps * 32) kv_attn_combine_kernel(const __grid_constant__ KvAttnParams p) {
   constexpr int E = D / 32, ROWS = 8 * NT;       // channels per lane
   __shared__ float part[kKaJoinWarps][D];
   __shared__ float lpart[kKaJoinWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 job = p.ws_meta[blockIdx.x];        // sequence, head and row tile, parts that share it
-  if (job.w == 0) return;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, row = blockIdx.y;
+  const int4 job = p.ws_meta[blockIdx.x];
+  if (job.w < 0) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, row = blockIdx.y, pieces = job.w - job.z + 1;
   const int kvh = job.y / p.row_tiles, r = (job.y - kvh * p.row_tiles) * ROWS + row, b = job.x;
   if (r >= p.R) return;
-  // piece 0: the end of the part before the cut; piece i: the beginning of part blockIdx.x - 1 + i
-  auto piece = [&](int i) -> int64_t { return ((int64_t)(blockIdx.x - 1 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
+  // piece 0: the end of the part that begins the job; piece i: the beginning of the i-th part after it
+  auto piece = [&](int i) -> int64_t { return ((int64_t)(job.z + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
   float mm = -INFINITY;
-  for (int i = lane; i < job.z; i += 32) mm = fmaxf(mm, p.ws_ml[piece(i)].x);
+  for (int i = lane; i < pieces; i += 32) mm = fmaxf(mm, p.ws_ml[piece(i)].x);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, k));
   const float ms = finite_or_zero(mm);
@@ -1122,7 +1125,7 @@ __global__ void __launch_bounds__(kKaJoinWarps * 32) kv_attn_combine_kernel(cons
 #pragma unroll
   for (int k = 0; k < E; ++k) s[k] = 0.0f;
 #pragma unroll 4
-  for (int i = w; i < job.z; i += kKaJoinWarps) {
+  for (int i = w; i < pieces; i += kKaJoinWarps) {
     const int64_t at = piece(i);
     const float2 st = p.ws_ml[at];
     const float f = ex2(st.x - ms);
