@@ -38,8 +38,8 @@
 // * the reference that numerators are taken against follows the maximum only when a score passes it by 2^5, so almost
 //   no tile rescales the accumulators;
 // * one job per CTA leaves SMs idle when sequences differ in length: all tokens of the call are cut evenly instead
-//   (see ka_units).  One sequence of 32768 tokens: 19.9 us; 48 of up to 8191: 47.2; 8 draft steps of 4 tokens,
-//   D = 64: 13.7; D = 256 with 16 query heads on one K/V head: 35.7; 301 tokens: 8.4 (of which launch, the query's
+//   (see ka_units).  One sequence of 32768 tokens: 18.3 us; 48 of up to 8191: 46.8; 8 draft steps of 4 tokens,
+//   D = 64: 13.5; D = 256 with 16 query heads on one K/V head: 35.7; 301 tokens: 8.4 (of which launch, the query's
 //   rotation and three dependent rounds of loads are most).
 #pragma once
 
@@ -1107,7 +1107,7 @@ template <int D, int NT, bool QBF>
 __global__ void __launch_bounds__(kKaJoinWarps * 32) kv_attn_combine_kernel(const __grid_constant__ KvAttnParams p) {
   constexpr int E = D / 32, ROWS = 8 * NT;       // channels per lane
   __shared__ float part[kKaJoinWarps][D];
-  __shared__ float lpart[kKaJoinWarps];
+  __shared__ float2 stat[kKaJoinWarps];          // the warps' references and denominators
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = p.ws_meta[blockIdx.x];
   if (job.w < 0) return;
@@ -1116,40 +1116,62 @@ __global__ void __launch_bounds__(kKaJoinWarps * 32) kv_attn_combine_kernel(cons
   if (r >= p.R) return;
   // piece 0: the end of the part that begins the job; piece i: the beginning of the i-th part after it
   auto piece = [&](int i) -> int64_t { return ((int64_t)(job.z + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
-  float mm = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) mm = fmaxf(mm, p.ws_ml[piece(i)].x);
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, k));
-  const float ms = finite_or_zero(mm);
-  float s[E], ll = 0.0f;
+  // every warp its pieces under its own maximum, statistics and sums fetched together: one round trip, not two (one long
+  // sequence 19.9 -> 18.3 us)
+  float m = -INFINITY, l = 0.0f, s[E];
 #pragma unroll
   for (int k = 0; k < E; ++k) s[k] = 0.0f;
-#pragma unroll 4
-  for (int i = w; i < pieces; i += kKaJoinWarps) {
-    const int64_t at = piece(i);
-    const float2 st = p.ws_ml[at];
-    const float f = ex2(st.x - ms);
-    ll = fmaf(st.y, f, ll);
-    float v[E];
+  for (int i = w; i < pieces; i += 4 * kKaJoinWarps) {
+    float2 st[4];
+    float v[4][E];
 #pragma unroll
-    for (int k = 0; k < E; k += 2) *reinterpret_cast<float2*>(v + k) = *reinterpret_cast<const float2*>(p.ws_o + at * D + lane * E + k);
+    for (int j = 0; j < 4; ++j) {
+      const int at = i + j * kKaJoinWarps;
+      st[j] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-    for (int k = 0; k < E; ++k) s[k] = fmaf(v[k], f, s[k]);
+      for (int k = 0; k < E; ++k) v[j][k] = 0.0f;
+      if (at < pieces) {
+        st[j] = p.ws_ml[piece(at)];
+#pragma unroll
+        for (int k = 0; k < E; k += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(p.ws_o + piece(at) * D + lane * E + k);
+          v[j][k] = x.x, v[j][k + 1] = x.y;
+        }
+      }
+    }
+    const float mn = fmaxf(m, fmaxf(fmaxf(st[0].x, st[1].x), fmaxf(st[2].x, st[3].x))), ms = finite_or_zero(mn);
+    const float f = ex2(m - ms);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) s[k] *= f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float fj = ex2(st[j].x - ms);
+      l = fmaf(st[j].y, fj, l);
+#pragma unroll
+      for (int k = 0; k < E; ++k) s[k] = fmaf(v[j][k], fj, s[k]);
+    }
   }
 #pragma unroll
   for (int k = 0; k < E; ++k) part[w][lane * E + k] = s[k];
-  if (lane == 0) lpart[w] = ll;
+  if (lane == 0) stat[w] = make_float2(m, l);
   __syncthreads();
-  ll = 0.0f;
+  float mm = -INFINITY, ll = 0.0f, fw[kKaJoinWarps];
 #pragma unroll
-  for (int k = 0; k < kKaJoinWarps; ++k) ll += lpart[k];
+  for (int k = 0; k < kKaJoinWarps; ++k) mm = fmaxf(mm, stat[k].x);
+#pragma unroll
+  for (int k = 0; k < kKaJoinWarps; ++k) {
+    fw[k] = ex2(stat[k].x - finite_or_zero(mm));
+    ll = fmaf(stat[k].y, fw[k], ll);
+  }
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
   const int i = r / p.G, hq = kvh * p.G + r % p.G;
   const int64_t at = b * p.o_sb + hq * p.o_sh + i * p.o_st;
   for (int d = threadIdx.x; d < D; d += kKaJoinWarps * 32) {
     float x = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kKaJoinWarps; ++k) x += part[k][d];
+    for (int k = 0; k < kKaJoinWarps; ++k) x = fmaf(part[k][d], fw[k], x);
     ka_store<QBF>(p.out, at + d, x * inv);
   }
   if (threadIdx.x == 0 && p.lse)
