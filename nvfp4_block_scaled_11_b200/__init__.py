@@ -145,6 +145,13 @@ def _out(t: torch.Tensor, name: str, dtype, need: int) -> torch.Tensor:
     return t
 
 
+def _one_device(dev: torch.device, **tensors) -> None:
+    """Every tensor of a launch is on the device that it runs on: a kernel given another device's memory faults."""
+    for name, t in tensors.items():
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -464,6 +471,7 @@ def kv_gscale(k: torch.Tensor, sink: int = 16, recent: int = 16, rotate: bool = 
         raise TypeError("k must be a 4-D bfloat16 tensor [B,H,T,D]")
     B, H, T, D = k.shape
     out = torch.empty(1, dtype=torch.float32, device=k.device) if out is None else _out(out, "out", torch.float32, 1)
+    _one_device(k.device, out=out)
     _check(lib().nvfp4_kv_gscale(_ptr(k), B, H, T, D, sink, recent, int(bool(rotate)), _ptr(out), _stream(k)))
     return out
 
@@ -483,6 +491,7 @@ def kv_append(k_rows: torch.Tensor, first: int, n: int, gscale: torch.Tensor, co
     cap = codes.shape[-2]
     _out(gscale, "gscale", torch.float32, 1), _out(codes, "codes", torch.uint8, BH * cap * (D // 2))
     _out(scales, "scales", torch.uint8, sf_mma_bytes(cap, D, BH) if tile_layout else BH * cap * (D // 16))
+    _one_device(k_rows.device, gscale=gscale, codes=codes, scales=scales)
     _check(lib().nvfp4_kv_append(_ptr(k_rows), BH, T, first, n, D, int(bool(rotate)), f_lo, f_hi, _ptr(gscale),
                                  _ptr(codes), _ptr(scales), cap, t0, 1 if tile_layout else 0, _stream(k_rows)))
 
