@@ -472,7 +472,7 @@ def kv_gscale(k: torch.Tensor, sink: int = 16, recent: int = 16, rotate: bool = 
     B, H, T, D = k.shape
     out = torch.empty(1, dtype=torch.float32, device=k.device) if out is None else _out(out, "out", torch.float32, 1)
     _one_device(k.device, out=out)
-    _check(lib().nvfp4_kv_gscale(_ptr(k), B, H, T, D, sink, recent, int(bool(rotate)), _ptr(out), _stream(k)))
+    _launch(k.device, lib().nvfp4_kv_gscale, _ptr(k), B, H, T, D, sink, recent, int(bool(rotate)), _ptr(out))
     return out
 
 
@@ -492,8 +492,8 @@ def kv_append(k_rows: torch.Tensor, first: int, n: int, gscale: torch.Tensor, co
     _out(gscale, "gscale", torch.float32, 1), _out(codes, "codes", torch.uint8, BH * cap * (D // 2))
     _out(scales, "scales", torch.uint8, sf_mma_bytes(cap, D, BH) if tile_layout else BH * cap * (D // 16))
     _one_device(k_rows.device, gscale=gscale, codes=codes, scales=scales)
-    _check(lib().nvfp4_kv_append(_ptr(k_rows), BH, T, first, n, D, int(bool(rotate)), f_lo, f_hi, _ptr(gscale),
-                                 _ptr(codes), _ptr(scales), cap, t0, 1 if tile_layout else 0, _stream(k_rows)))
+    _launch(k_rows.device, lib().nvfp4_kv_append, _ptr(k_rows), BH, T, first, n, D, int(bool(rotate)), f_lo, f_hi, _ptr(gscale),
+            _ptr(codes), _ptr(scales), cap, t0, 1 if tile_layout else 0)
 
 
 class _KvAppendDesc(ctypes.Structure):
@@ -550,8 +550,7 @@ class KvAppendBatch:
             d[i].first = int(first if one[0] else first[i])
             d[i].n = int(n if one[1] else n[i])
             d[i].t0 = int(t0 if one[2] else t0[i])
-        _check(lib().nvfp4_kv_append_batch(ctypes.cast(d, _P), self._count, self.f_lo, self.f_hi,
-                                           ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)))
+        _launch(self._device, lib().nvfp4_kv_append_batch, ctypes.cast(d, _P), self._count, self.f_lo, self.f_hi)
 
 
 def kv_append_batch(items, f_lo: int = -2, f_hi: int = 6) -> None:

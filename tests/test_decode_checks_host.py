@@ -46,3 +46,13 @@ def test_quantizing_calls_refuse_tensors_of_another_device(launches):
         with pytest.raises(ValueError, match="is on"):
             nv.kv_append(a["k"], 0, 16, a["g"], a["codes"], a["scales"], 0)
     assert not launches
+
+
+def test_quantizing_calls_run_on_their_tensors_device(launches):
+    """Whatever device is current: the launch goes through the one place that switches to the tensors' device."""
+    k, g = torch.zeros(1, 2, 40, 32, dtype=BF), torch.zeros(1)
+    codes, scales = torch.zeros(1, 2, 64, 16, dtype=torch.uint8), torch.zeros(1, 2, 64, 2, dtype=torch.uint8)
+    nv.kv_gscale(k, 4, 4, out=g)
+    nv.kv_append(k, 0, 16, g, codes, scales, 0)
+    nv.KvAppendBatch([(k, g, codes, scales, True, False)])(0, 16, 0)
+    assert launches == [(k.device, n) for n in ("nvfp4_kv_gscale", "nvfp4_kv_append", "nvfp4_kv_append_batch")]
