@@ -452,9 +452,13 @@ class NVFP4PagedKVCache:
         return self._held[slot]
 
     def _prompt(self, x: torch.Tensor) -> torch.Tensor:
-        x = x if x.dim() == 4 else x[None]
-        if x.shape[:2] != (1, self.H) or x.shape[3] != self.D or x.dtype != torch.bfloat16:
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("prompts must be tensors")
+        x = x[None] if x.dim() == 3 else x
+        if x.dim() != 4 or x.shape[:2] != (1, self.H) or x.shape[3] != self.D or x.dtype != torch.bfloat16:
             raise ValueError("prompts must be bfloat16 [H, T, D] matching the cache")
+        if x.device != self.device:                # its address goes to a kernel on the cache's device
+            raise ValueError(f"a prompt is on {x.device}, the cache on {self.device}")
         return x.contiguous()
 
     def _take(self) -> int:

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import nvfp4_block_scaled_11_b200 as nv
+import nvfp4_block_scaled_11_b200.kvcache as kc
 
 BF = torch.bfloat16
 
@@ -56,3 +57,47 @@ def test_quantizing_calls_run_on_their_tensors_device(launches):
     nv.kv_append(k, 0, 16, g, codes, scales, 0)
     nv.KvAppendBatch([(k, g, codes, scales, True, False)])(0, 16, 0)
     assert launches == [(k.device, n) for n in ("nvfp4_kv_gscale", "nvfp4_kv_append", "nvfp4_kv_append_batch")]
+
+
+# ---- the paged cache ----
+H, D, PAGE = 2, 32, 32
+
+
+@pytest.fixture
+def log(monkeypatch):
+    """What the cache would launch; `fail` names the call that raises instead."""
+    out = dict(append=[], copies=[], fail=None)
+
+    def call(name, *a):
+        if out["fail"] == name:
+            raise RuntimeError("launch")
+        out.setdefault(name, []).append(a)
+    monkeypatch.setattr(kc, "_append_records", lambda recs, lo, hi, dev: call("append", recs.copy()))
+    monkeypatch.setattr(kc, "kv_gscale", lambda k, s, r, rot, out: call("gscale") or out.fill_(0.5))
+    monkeypatch.setattr(kc, "copy_pages", lambda arrays, src, dst: call("copies", list(src), list(dst)))
+    return out
+
+
+def _cache(pages=12, slots=4, layers=2, **kw):
+    return kc.NVFP4PagedKVCache(layers, slots, H, D, pages, PAGE, device="cpu", **kw)
+
+
+def _prompt(T, layers=2):
+    return [torch.zeros(H, T, D, dtype=BF) for _ in range(layers)]
+
+
+def test_prompts_on_another_device_are_refused(log):
+    c = _cache()
+    s = c.alloc()
+    good, away = _prompt(100), [x.to("meta") for x in _prompt(100)]
+    for ks, vs in ((away, good), (good, away), (good, [good[0], away[1]])):
+        with pytest.raises(ValueError, match="on meta"):
+            c.prefill(s, ks, vs)
+    for bad in (1.0, None, [0.0]):
+        with pytest.raises(TypeError):
+            c.prefill(s, [bad, bad], good)
+    with pytest.raises(ValueError):
+        c.prefill(s, [x[0] for x in good], good)                     # no heads
+    assert c.pages_free == 12 and c.length(s) == 0
+    c.prefill(s, good, good)
+    assert c.length(s) == 100
