@@ -297,11 +297,10 @@ class NVFP4PagedKVCache:
 
     def free(self, slot: int) -> None:
         """End a sequence: its slot and the pages that no other sequence shares are free again."""
-        for p in self._owned(slot):
-            self._drop(p)
+        self._owned(slot)
+        self._release(slot)
         self._held[slot] = None
         self._lens[slot] = 0
-        self._table[slot] = -1
         self._publish([slot])
 
     def prefill(self, slot: int, ks, vs) -> None:
@@ -318,18 +317,22 @@ class NVFP4PagedKVCache:
             raise ValueError("prefill needs at least sink + recent tokens")
         mid = T - s - r
         self._grow([(slot, mid)])
-        for side, xs in enumerate(sides):
-            for layer, x in enumerate(xs):
-                # a prompt without a middle sets the scale by all of its tokens (0 would quantize every later one to 0)
-                kv_gscale(x, s if mid else 0, r if mid else 0, self.rotate, out=self.gscale[layer, side, slot:slot + 1])
-                self.sink[layer, side, slot].copy_(x[0, :, :s])
-                self.window[layer, side, slot, :, :r].copy_(x[0, :, T - r:])
-        P = self.page_tokens
-        rows = [(slot, s + i * P, min(P, mid - i * P), p, 0) for i, p in enumerate(self._held[slot])]
-        for side, xs in enumerate(sides):
-            for layer, x in enumerate(xs):
-                if rows:
-                    self._quantize(rows, layer, side, x.data_ptr(), 0, T)
+        try:
+            for side, xs in enumerate(sides):
+                for layer, x in enumerate(xs):
+                    # a prompt without a middle sets the scale by all of its tokens (0 would quantize every later one to 0)
+                    kv_gscale(x, s if mid else 0, r if mid else 0, self.rotate, out=self.gscale[layer, side, slot:slot + 1])
+                    self.sink[layer, side, slot].copy_(x[0, :, :s])
+                    self.window[layer, side, slot, :, :r].copy_(x[0, :, T - r:])
+            P = self.page_tokens
+            rows = [(slot, s + i * P, min(P, mid - i * P), p, 0) for i, p in enumerate(self._held[slot])]
+            for side, xs in enumerate(sides):
+                for layer, x in enumerate(xs):
+                    if rows:
+                        self._quantize(rows, layer, side, x.data_ptr(), 0, T)
+        except BaseException:                      # the sequence stays empty and holds nothing
+            self._release(slot)
+            raise
         self._lens[slot] = (s, mid, 0, r)
         self._publish([slot])
 
@@ -470,6 +473,13 @@ class NVFP4PagedKVCache:
         self._refs[p] -= 1
         if not self._refs[p]:
             heapq.heappush(self._free, p)
+
+    def _release(self, slot: int) -> None:
+        """The sequence's pages back to the pool (those that no other one shares)."""
+        for p in self._held[slot]:
+            self._drop(p)
+        self._held[slot].clear()
+        self._table[slot] = -1
 
     def _grow(self, wants) -> None:
         """Pages for middles of the given tokens, all or none."""

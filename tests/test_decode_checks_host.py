@@ -101,3 +101,17 @@ def test_prompts_on_another_device_are_refused(log):
     assert c.pages_free == 12 and c.length(s) == 0
     c.prefill(s, good, good)
     assert c.length(s) == 100
+
+
+@pytest.mark.parametrize("call", ["gscale", "append"])
+def test_a_prefill_that_fails_gives_its_pages_back(log, call):
+    c = _cache()
+    a, s = c.alloc(), c.alloc()
+    c.prefill(a, _prompt(100), _prompt(100))
+    log["fail"] = call
+    with pytest.raises(RuntimeError, match="launch"):
+        c.prefill(s, _prompt(32 + 40), _prompt(32 + 40))
+    assert c.pages_free == 12 - 3 and c.length(s) == 0 and c._held[s] == [] and (c._table[s] == -1).all()
+    log["fail"] = None
+    c.prefill(s, _prompt(32 + 40), _prompt(32 + 40))                 # the slot can be used again at once
+    assert c.length(s) == 72 and c.table[s, :3].tolist() == [3, 4, -1]
