@@ -406,16 +406,17 @@ class NVFP4PagedKVCache:
                 raise RuntimeError("prefill first")
         full = [s for s in slots if self._lens[s, 3] + n > 2 * r]
         self._grow([(s, int(self._lens[s, 1]) + r) for s in full])
-        rows, P = [], self.page_tokens
+        rows, flushed, P = [], [], self.page_tokens
         for s in full:
             first, mid, left = int(self._lens[s, 2]), int(self._lens[s, 1]), r
             while left:                                      # a group may cross pages
                 k = min(left, P - mid % P)
                 rows.append((s, first, k, self._held[s][mid // P], mid % P))
                 first, mid, left = first + k, mid + k, left - k
-            self._lens[s] = (self._lens[s, 0], mid, (self._lens[s, 2] + r) % (2 * r), self._lens[s, 3] - r)
+            flushed.append((self._lens[s, 0], mid, (self._lens[s, 2] + r) % (2 * r), self._lens[s, 3] - r))
         if rows:
             self._quantize(rows, None, None, self.window.data_ptr(), self.H * 2 * r * self.D * 2, 2 * r)
+            self._lens[full] = flushed               # only now: a step that fails can be made again
         head = (self._lens[slots, 2] + self._lens[slots, 3]).astype(np.int64)
         self._lens[slots, 3] += n
         self._publish(slots)

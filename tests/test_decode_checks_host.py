@@ -115,3 +115,20 @@ def test_a_prefill_that_fails_gives_its_pages_back(log, call):
     log["fail"] = None
     c.prefill(s, _prompt(32 + 40), _prompt(32 + 40))                 # the slot can be used again at once
     assert c.length(s) == 72 and c.table[s, :3].tolist() == [3, 4, -1]
+
+
+def test_a_step_whose_flush_fails_can_be_made_again(log):
+    c = _cache()
+    s = c.alloc()
+    c.prefill(s, _prompt(32 + 24), _prompt(32 + 24))
+    for _ in range(16):
+        c.step([s])
+    before, log["fail"] = c._lens.copy(), "append"
+    with pytest.raises(RuntimeError, match="launch"):
+        c.step([s])
+    assert (c._lens == before).all() and c.length(s) == 72
+    log["fail"], log["append"] = None, []
+    c.step([s])
+    ((recs,),) = log["append"]
+    assert recs["first"].tolist() == [0, 8] * 4 and recs["t0"].tolist() == [24, 0] * 4
+    assert c.lens[s].tolist() == [16, 40, 16, 17]
