@@ -427,9 +427,12 @@ class NVFP4PagedKVCache:
     def store(self, step: DecodeStep, layer: int, k: torch.Tensor, v: torch.Tensor) -> None:
         """The step's K and V rows [B, H, n, D] (BF16) of one layer."""
         shape = (len(step.slots), self.H, step.n, self.D)
+        if not 0 <= layer < self.layers:
+            raise IndexError("no such layer")
+        for x in (k, v):                             # both before the first is written
+            if x.shape != shape or x.dtype != torch.bfloat16 or x.device != self.device:
+                raise ValueError(f"k and v must be bfloat16 {list(shape)} on {self.device}")
         for side, x in enumerate((k, v)):
-            if x.shape != shape or x.dtype != torch.bfloat16:
-                raise ValueError(f"k and v must be bfloat16 {list(shape)}")
             self.window[layer, side][step._rows, :, step._at] = x.transpose(1, 2)
 
     def attend(self, step: DecodeStep, layer: int, q: torch.Tensor, scale: float | None = None, causal: bool = True,

@@ -132,3 +132,19 @@ def test_a_step_whose_flush_fails_can_be_made_again(log):
     ((recs,),) = log["append"]
     assert recs["first"].tolist() == [0, 8] * 4 and recs["t0"].tolist() == [24, 0] * 4
     assert c.lens[s].tolist() == [16, 40, 16, 17]
+
+
+def test_refused_rows_are_not_stored(log):
+    """Neither side's when one is refused, and no layer's that there is not (-1 is not the last one)."""
+    c = _cache()
+    s = c.alloc()
+    c.prefill(s, _prompt(40), _prompt(40))
+    st, before = c.step([s]), c.window.clone()
+    x = torch.ones(1, H, 1, D, dtype=BF)
+    for k, v in ((x, x[:, :1]), (x, x.float()), (x, x.to("meta")), (x[:, :, :0], x)):
+        with pytest.raises(ValueError):
+            c.store(st, 0, k, v)
+    for layer in (-1, 2):
+        with pytest.raises(IndexError):
+            c.store(st, layer, x, x)
+    assert torch.equal(c.window, before)
