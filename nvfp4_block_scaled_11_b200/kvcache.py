@@ -16,7 +16,8 @@ caches of every layer for many sequences of different lengths over one pool of p
 were forked share.
 
 Host-side bookkeeping only: token rows are moved with tensor copies, every quantization, attention and page
-copy runs in the library's kernels.
+copy runs in the library's kernels.  The caches keep values, not gradients: rows that require them are detached, and
+attention over a cache returns tensors without.
 """
 from __future__ import annotations
 
@@ -83,7 +84,7 @@ class NVFP4KVCache:
         s, r = self.n_sink_max, self.recent
         if T < s + r:
             raise ValueError("prefill needs at least sink + recent tokens")
-        k = k.contiguous()
+        k = k.detach().contiguous()
         n_mid = T - s - r
         if n_mid > self.capacity:
             raise ValueError("prefill middle exceeds the cache capacity")
@@ -126,7 +127,7 @@ class NVFP4KVCache:
 
     def _push(self, token: torch.Tensor) -> None:
         slot = (self.head + self.n_window) % (2 * self.recent)
-        self.window[:, :, slot].copy_(token)
+        self.window[:, :, slot].copy_(token.detach())
         self.n_window += 1
 
     def recent_tokens(self) -> torch.Tensor:
@@ -433,7 +434,7 @@ class NVFP4PagedKVCache:
             if x.shape != shape or x.dtype != torch.bfloat16 or x.device != self.device:
                 raise ValueError(f"k and v must be bfloat16 {list(shape)} on {self.device}")
         for side, x in enumerate((k, v)):
-            self.window[layer, side][step._rows, :, step._at] = x.transpose(1, 2)
+            self.window[layer, side][step._rows, :, step._at] = x.detach().transpose(1, 2)
 
     def attend(self, step: DecodeStep, layer: int, q: torch.Tensor, scale: float | None = None, causal: bool = True,
                want_lse: bool = False, out: torch.Tensor | None = None):
@@ -466,7 +467,7 @@ class NVFP4PagedKVCache:
             raise ValueError("prompts must be bfloat16 [H, T, D] matching the cache")
         if x.device != self.device:                # its address goes to a kernel on the cache's device
             raise ValueError(f"a prompt is on {x.device}, the cache on {self.device}")
-        return x.contiguous()
+        return x.detach().contiguous()
 
     def _take(self) -> int:
         p = heapq.heappop(self._free)

@@ -148,3 +148,18 @@ def test_refused_rows_are_not_stored(log):
         with pytest.raises(IndexError):
             c.store(st, layer, x, x)
     assert torch.equal(c.window, before)
+
+
+def test_caches_hold_no_graph(log):
+    """Rows of a projection whose weights train: the buffers stay plain, so no graph grows with the sequence."""
+    c = _cache()
+    s = c.alloc()
+    p = [x.requires_grad_() for x in _prompt(40)]
+    c.prefill(s, p, p)
+    x = torch.ones(1, H, 1, D, dtype=BF, requires_grad=True)
+    c.store(c.step([s]), 1, x, x * 2)
+    assert not c.window.requires_grad and not c.sink.requires_grad and c.window[1, 1, s, 0, 16, 0] == 2
+    one = kc.NVFP4KVCache(1, H, D, capacity=16, device="cpu")
+    one.prefill(p[0][None][:, :, :32])
+    one.append(x)
+    assert not one.window.requires_grad and not one.sink.requires_grad and one.length == 33
