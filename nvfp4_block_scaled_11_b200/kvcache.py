@@ -31,6 +31,12 @@ from . import (KV_APPEND_BATCH_MAX, KvAppendBatch, KvStore, _KvAppendDesc, _laun
                kv_gscale, lib, sf_mma_bytes)
 
 
+def _buffers(c) -> tuple:
+    """Where a cache's buffers are: its KvStores are made anew when one has been replaced.  (A KvStore keeps what it reads
+    alive, so a replacement never has the old one's address.)"""
+    return (*(t.data_ptr() for t in (c.sink, c.window, c.codes, c.scales, c.gscale)), c.rotate)
+
+
 class NVFP4KVCache:
     """K (or V) cache of B x H heads of dimension D with room for `capacity` NVFP4 middle tokens.
 
@@ -63,12 +69,14 @@ class NVFP4KVCache:
         self.head = 0        # first valid window slot: 0 or recent
         self.n_window = 0
         self.prefilled = False
-        self._store = None
+        self._store = self._store_of = None
 
     def store(self) -> KvStore:
-        """The cache as kv_attention reads it."""
-        if self._store is None:
+        """The cache as kv_attention reads it, made once for the buffers that the cache has now."""
+        of = _buffers(self)
+        if self._store_of != of:
             self._store = KvStore(self.sink, self.window, self.codes, self.scales, self.gscale, self.rotate, self.tile_layout)
+            self._store_of = of
         return self._store
 
     @property
@@ -278,6 +286,7 @@ class NVFP4PagedKVCache:
         self._refs = [0] * pages
         self._free = list(range(pages))                    # a heap: the lowest page first
         self._stores: dict[int, tuple[KvStore, KvStore]] = {}
+        self._stores_of = None
 
     # ---- sequences ----
     @property
@@ -446,6 +455,9 @@ class NVFP4PagedKVCache:
 
     def stores(self, layer: int) -> tuple[KvStore, KvStore]:
         """The layer's K and V as kv_attention reads them (with `lens` and `table`)."""
+        of = _buffers(self)
+        if self._stores_of != of:                    # buffers were replaced (or none was asked for yet)
+            self._stores, self._stores_of = {}, of
         if layer not in self._stores:
             if not 0 <= layer < self.layers:
                 raise IndexError("no such layer")

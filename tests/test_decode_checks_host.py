@@ -163,3 +163,19 @@ def test_caches_hold_no_graph(log):
     one.prefill(p[0][None][:, :, :32])
     one.append(x)
     assert not one.window.requires_grad and not one.sink.requires_grad and one.length == 33
+
+
+def test_replaced_buffers_are_read(monkeypatch):
+    """A cache whose buffer is replaced gives attention the new one, and the same view again while none is."""
+    monkeypatch.setattr(kc, "KvStore", lambda *a: a)
+    one, many = kc.NVFP4KVCache(1, H, D, capacity=16, device="cpu"), _cache()
+    for c, get in ((one, one.store), (many, lambda: many.stores(1)[1])):
+        for i, name in enumerate(("sink", "window", "codes", "scales", "gscale")):
+            old = get()
+            assert get() is old
+            setattr(c, name, getattr(c, name).clone())
+            new = get()
+            assert [a.data_ptr() == b.data_ptr() for a, b in zip(old[:5], new[:5])] == [j != i for j in range(5)]
+        old = get()
+        c.codes.data = c.codes.clone()
+        assert get()[2].data_ptr() != old[2].data_ptr()
