@@ -397,7 +397,8 @@ typedef struct nvfp4_kv_store {
   const uint8_t* codes;     /* NVFP4 middle [pages, Hkv, page_rows, D/2]; 16-byte aligned */
   const uint8_t* scales;    /* [pages, Hkv, page_rows, D/16], or pages * Hkv matrices [page_rows, D] in the tile
                                layout when scale_layout == 1; 4-byte aligned */
-  const float* gscale;      /* the tensor scale: one float, or one per slot when gscale_stride == 1 */
+  const float* gscale;      /* the tensor scale: one float, or one per slot when gscale_stride == 1; needed wherever a
+                               middle may have tokens, also when all of their pages lie outside the pool */
   int64_t gscale_stride;    /* 0 or 1 */
   int32_t rotate;           /* 1: the middle is rotated by FWHT-16 along D (undone by the attention) */
   int32_t scale_layout;

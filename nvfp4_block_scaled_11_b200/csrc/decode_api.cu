@@ -73,13 +73,15 @@ int ka_row_units(int64_t rows) { return rows <= 8 ? 1 : 2; }
 // CTAs of the attention kernel that an SM holds (its launch bounds and shared memory).
 int ka_ctas_per_sm(int64_t D, int nt) { return D == 256 ? 2 : D == 128 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 4 : 3); }
 
-// One side of the cache: pointers and layout into the kernel's form.
+// One side of the cache: pointers and layout into the kernel's form.  mid_rows: the longest middle that a sequence may
+// have.  Its tensor scale is read even where all of its pages lie outside the pool (pages == 0: tokens that count but
+// are hidden); codes and scales are not.
 int ka_side(const nvfp4_kv_store& c, const nvfp4_kv_attention_desc& d, int64_t mid_rows, KvSide& o) {
   if ((c.rotate != 0 && c.rotate != 1) || (c.scale_layout != 0 && c.scale_layout != 1) ||
       (c.gscale_stride != 0 && c.gscale_stride != 1))
     return NVFP4_ERR_ARG;
   if ((d.sink_rows > 0 && c.sink == nullptr) || (d.window_rows > 0 && c.window == nullptr) ||
-      (mid_rows > 0 && (c.codes == nullptr || c.scales == nullptr || c.gscale == nullptr)))
+      (mid_rows > 0 && (c.gscale == nullptr || (d.pages > 0 && (c.codes == nullptr || c.scales == nullptr)))))
     return NVFP4_ERR_ARG;
   if (!aligned(c.sink, 16) || !aligned(c.window, 16) || !aligned(c.codes, 16) || !aligned(c.scales, 4) || !aligned(c.gscale, 4))
     return NVFP4_ERR_ALIGN;
@@ -162,8 +164,8 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* wo
       !aligned(d.lens, 4) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
   KvAttnParams p{};
-  if (int rc = ka_side(d.k, d, d.pages > 0 ? mid_rows : 0, p.k)) return rc;
-  if (int rc = ka_side(d.v, d, d.pages > 0 ? mid_rows : 0, p.v)) return rc;
+  if (int rc = ka_side(d.k, d, mid_rows, p.k)) return rc;
+  if (int rc = ka_side(d.v, d, mid_rows, p.v)) return rc;
   const int64_t G = d.Hq / d.Hkv, R = checked_prod({G, d.Tq});
   if (R < 0 || R > kMaxInt) return NVFP4_ERR_SIZE;
   const int nt = ka_row_units(R);

@@ -1,10 +1,13 @@
 """Decode cache and its calls without a GPU: tensors on other devices, refused calls that change nothing.  Launches are
 replaced by recorders; a `meta` tensor stands for one on another device."""
+import ctypes
+
 import pytest
 import torch
 
 import nvfp4_block_scaled_11_b200 as nv
 import nvfp4_block_scaled_11_b200.kvcache as kc
+from nvfp4_block_scaled_11_b200 import build as nvbuild
 
 BF = torch.bfloat16
 
@@ -179,3 +182,37 @@ def test_replaced_buffers_are_read(monkeypatch):
         old = get()
         c.codes.data = c.codes.clone()                               # the same tensor, its memory moved
         assert get() is not old and get() is get()
+
+
+# ---- the C entry points, on fake pointers: everything here is decided on the host ----
+ARG, SIZE = -1, -2
+
+
+@pytest.fixture(scope="module")
+def L():
+    nvbuild.build()
+    return nv.lib()
+
+
+def _desc(k=None, v=None, **kw):
+    store = dict(sink=0x10000, window=0x20000, codes=0x30000, scales=0x40000, gscale=0x50000, gscale_stride=0, rotate=1,
+                 scale_layout=0)
+    d = nv._KvAttentionDesc()
+    for name, x in (dict(q=0x60000, out=0x70000, B=1, Hq=8, Hkv=2, Tq=1, D=128, slots=1, sink_rows=16, window_rows=32, pages=4,
+                         page_rows=64, n_sink=16, n_window=16, dtype=1, causal=1, scale=0.1) | kw).items():
+        setattr(d, name, x)
+    for name, s in (("k", store | (k or {})), ("v", store | (v or {}))):
+        setattr(d, name, nv._KvStore(*(s[f] for f, _ in nv._KvStore._fields_)))
+    return d
+
+
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_a_pool_without_pages_still_needs_the_tensor_scale(L, side):
+    """Tokens of pages outside the pool are hidden, but the kernel reads their sequence's tensor scale."""
+    paged = dict(table=0x80000, table_cols=4, lens=0x90000)
+    for kw in (dict(pages=0), dict(pages=4)):
+        assert L.nvfp4_kv_attention(ctypes.byref(_desc(**{side: dict(gscale=None)}, **paged, **kw)), 1, None, 0, None) == ARG
+    # nothing to read where no middle can be: past the check of the stores, to a size that is refused after it
+    none = dict(paged, table_cols=0, pages=0, Hq=1 << 30, Hkv=1, Tq=4)
+    assert L.nvfp4_kv_attention(ctypes.byref(_desc(**{side: dict(gscale=None, codes=None, scales=None)}, **none)), 1, None, 0,
+                                None) == SIZE
