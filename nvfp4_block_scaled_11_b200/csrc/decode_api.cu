@@ -185,7 +185,8 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_desc* desc, int splits, void* wo
   p.page_shift = -1;
   if (d.page_rows > 0 && (d.page_rows & (d.page_rows - 1)) == 0) p.page_shift = __builtin_ctzll((unsigned long long)d.page_rows);
   p.slots = d.slots, p.pages = d.pages, p.cols = d.table_cols;
-  p.slot = d.slot, p.table = d.table, p.lens = d.lens;
+  p.slot = d.slot, p.table = d.table;
+  p.lens = d.slots > 0 ? d.lens : nullptr;             // the kernel reads slot 0's for an unknown slot: none there is not read
   p.host_lens[0] = d.n_sink, p.host_lens[1] = d.n_mid, p.host_lens[2] = d.head, p.host_lens[3] = d.n_window;
   p.B = (int)d.B;
   p.causal = d.causal;
