@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
           return;
         }
         if (tiles32 && (r0 & 31) == 0) {          // 32 rows of a scale tile: every fourth word of its 512 bytes
-          const uint64_t o = (uint64_t)((uint32_t)pg0 * (uint32_t)p.Hkv + kvh) * p.k.mat_bytes + (uint32_t)(r0 >> 7) * (D / 64 * 512) +
-                             4 * (r0 >> 5 & 3) + lane * 16;
+          const uint64_t o = (uint64_t)((uint32_t)pg0 * (uint32_t)p.Hkv + kvh) * p.k.mat_bytes +
+                             (uint64_t)(r0 >> 7) * (D / 64 * 512) + 4 * (r0 >> 5 & 3) + lane * 16;
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
             cp_async4(sa + lane * Sh::kScaleRow + 4 * j, p.k.scales + o + j * 512);

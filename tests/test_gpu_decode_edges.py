@@ -27,3 +27,29 @@ def test_no_slots_make_every_sequence_empty():
     assert nv.lib().nvfp4_kv_attention(ctypes.byref(d), 1, None, 0, torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_scale_tiles_past_32_bits():
+    """One sequence of more than 2^28 tokens of 256 channels, scales in tiles: its last tokens are read with their own scales
+    (those bytes begin at 2^32 of the matrix).  All tokens but the last 128 are zeros: scores 0, values 0."""
+    gen = torch.Generator().manual_seed(21)
+    D, n, far = 256, 128, 1 << 28
+    s = kvref.Side(gen, 1, 1, D, 0, 16, 1, n, rotate=False)
+    codes = torch.zeros(1, 1, far + n, D // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(nv.sf_mma_bytes(far + n, D, 1), dtype=torch.uint8, device="cuda")
+    codes[0, 0, far:], scales[-n * D // 16:] = s.codes[0, 0].cuda(), kvref.tile_scales(s.scales.flatten(0, 1)).cuda()
+    st = nv.KvStore(s.sink.cuda(), s.window.cuda(), codes, scales, s.gscale.cuda(), False, True)
+    val = s.tokens(0, (0, n, 0, 0), None)[0][0]                       # [128, 256] in 64 bits
+    q = (torch.randn(1, 2, 1, D, generator=gen) * 12).to(BF)
+    x = q[0, :, 0].double() @ val.T * D ** -0.5
+    assert x.max() > 20                                               # enough to be seen beside e^0 2^28 times
+    m = x.amax(1, keepdim=True)
+    p = torch.exp(x - m)
+    l = p.sum(1, keepdim=True) + far * torch.exp(-m)
+    want, mag = p @ val / l, p @ val.abs() / l
+    out, lse = nv.kv_attention(q.cuda(), st, st, (0, far + n, 0, 0), want_lse=True)
+    # FP32 scores of up to |x| and sums of the parts (2^28 tokens over at least 148 * 4 warps' 8 lanes a row), FP16 numerators
+    rel = float(2 * x.abs().max() * 2.0 ** -20 + (far / (148 * 32) + 64) * 2.0 ** -24)
+    assert ((out[0, :, 0].cpu().double() - want).abs() <= mag * (rel + 2.0 ** -11) + 2.0 ** -8 * want.abs() + 1e-9).all()
+    assert ((lse[0, :, 0].cpu().double() - (m + torch.log(l))[:, 0]).abs() <= rel + 2.0 ** -20).all()
+    assert want.abs().max() > 0.5
