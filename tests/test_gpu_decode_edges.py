@@ -53,3 +53,64 @@ def test_scale_tiles_past_32_bits():
     assert ((out[0, :, 0].cpu().double() - want).abs() <= mag * (rel + 2.0 ** -11) + 2.0 ** -8 * want.abs() + 1e-9).all()
     assert ((lse[0, :, 0].cpu().double() - (m + torch.log(l))[:, 0]).abs() <= rel + 2.0 ** -20).all()
     assert want.abs().max() > 0.5
+
+
+def _run(q, k, v, lens, table=None, slots=None, **kw):
+    dev = lambda t: None if t is None else torch.as_tensor(t, dtype=torch.int32).cuda()  # noqa: E731
+    out, lse = nv.kv_attention(q.cuda(), k.store(nv), v.store(nv), dev(lens), dev(table), dev(slots), want_lse=True, **kw)
+    torch.cuda.synchronize()
+    kvref.check(out, lse, kvref.attention(q, k, v, lens, table if table is None else torch.as_tensor(table), slots,
+                                          kw.get("causal", True)))
+    return out
+
+
+@pytest.mark.parametrize("tk,tv", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 48), (256, 16), (64, 32), (128, 64), (256, 128), (128, 160)])
+def test_scale_tiles_in_pages_and_on_one_side(D, page, tk, tv):
+    """Each page's scales in tiles of their own, for both sides or one: pages that end inside a tile, inside 32 rows of one,
+    and that hold several."""
+    gen = torch.Generator().manual_seed(D + page)
+    mids = [333, page, 0, 31]
+    need = [-(-m // page) for m in mids]
+    pages = sum(need) + 2
+    order = torch.randperm(pages, generator=gen).tolist()
+    table = torch.full((4, max(need)), -1, dtype=torch.int32)
+    for s, n in enumerate(need):
+        table[s, :n] = torch.tensor([order.pop() for _ in range(n)], dtype=torch.int32)
+    k, v = (kvref.Side(gen, 4, 2, D, 16, 32, pages, page, tile=t, per_slot=True) for t in (tk, tv))
+    _run((2 * torch.randn(4, 6, 1, D, generator=gen)).to(BF), k, v, [(16, m, 16, 17) for m in mids], table)
+
+
+@pytest.mark.parametrize("tk,tv", [(True, False), (False, True)])
+@pytest.mark.parametrize("D,cap", [(64, 129), (128, 300), (256, 130)])
+def test_scale_tiles_on_one_side_of_a_contiguous_cache(D, cap, tk, tv):
+    gen = torch.Generator().manual_seed(D + cap)
+    k, v = (kvref.Side(gen, 2, 2, D, 16, 32, 2, cap, tile=t) for t in (tk, tv))
+    _run((2 * torch.randn(2, 4, 2, D, generator=gen)).to(F16), k, v, [(16, cap, 0, 16), (3, cap - 1, 16, 32)])
+
+
+@pytest.mark.parametrize("B", [128, 129, 300])
+def test_more_sequences_than_threads_of_a_cta(B):
+    """Ragged batches whose rows are shared out to the threads that add their work up: one, two and three rows each, some
+    of them empty or of slots that do not exist."""
+    gen = torch.Generator().manual_seed(B)
+    k, v = (kvref.Side(gen, 40, 1, 64, 16, 32, 90, 32, per_slot=True) for _ in (0, 1))
+    table = torch.randint(0, 90, (40, 9), generator=gen).int()
+    lens = [(int(a), int(m), 0, int(w)) for a, m, w in zip(torch.randint(0, 17, (40,), generator=gen),
+                                                          torch.randint(0, 289, (40,), generator=gen) * torch.randint(0, 2, (40,), generator=gen),
+                                                          torch.randint(0, 33, (40,), generator=gen))]
+    slots = torch.randint(-1, 42, (B,), generator=gen).tolist()
+    q = (2 * torch.randn(B, 2, 1, 64, generator=gen)).to(BF)
+    a = _run(q, k, v, lens, table, slots, max_mid=288)
+    assert torch.equal(a, _run(q, k, v, lens, table, slots, max_mid=288))
+    _run(q, k, v, lens, table, slots, splits=5)
+
+
+@pytest.mark.parametrize("D,G,Tq,dt", [(256, 12, 3, BF), (256, 12, 3, F16), (256, 4, 8, F16), (256, 1, 17, BF), (128, 4, 4, F16),
+                                       (128, 16, 8, F16), (128, 3, 43, BF), (64, 8, 16, F16)])
+def test_many_query_rows(D, G, Tq, dt):
+    """Rows in several tiles of 16 and a rest, at every head_dim, for both types; the newest tokens in the window, in the
+    middle and in both."""
+    gen = torch.Generator().manual_seed(D + G * Tq)
+    k, v = (kvref.Side(gen, 3, 2, D, 16, 32, 3, 300, per_slot=True) for _ in (0, 1))
+    _run((1.5 * torch.randn(3, 2 * G, Tq, D, generator=gen)).to(dt), k, v, [(16, 270, 5, 32), (16, 299, 0, 2), (7, 0, 31, 9)])
