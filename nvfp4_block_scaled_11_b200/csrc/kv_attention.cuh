@@ -30,8 +30,10 @@
 //   140, since 128-token operands need their copies, fences and TMEM reads in step and the values still have to be
 //   expanded;
 // * the rotated query is split into two FP16 terms (22 bits after a power-of-two row scale), so scores
-//   keep FP32 accuracy; the numerators are rounded to FP16 once, scaled by 2^10 (2^-12 relative error
-//   each down to 2^-24 of the row's maximum; sums are taken in FP32 before that rounding);
+//   keep FP32 accuracy; the numerators are rounded to FP16 once, scaled by 2^10 (11 significant bits, so up to 2^-11
+//   relative error each, down to 2^-24 of the row's maximum; the denominators are FP32 sums taken before that
+//   rounding, so the error of a token that holds all the weight does not cancel: a second term of 11 bits would take a
+//   second product over the values);
 // * S^T = K Q^T leaves (token, query) fragments; movmatrix turns the FP16 numerators into the second
 //   product's operand; V is packed along channels, so pairs of tokens are interleaved nibble by nibble
 //   (two logic operations per 8 codes and token) before the converts;

@@ -1,6 +1,7 @@
 """Edges of attention over the cache and of the calls around it: pools and batches without entries, the far end of a long
 cache, layouts in combination, large batches, many query rows."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -114,3 +115,30 @@ def test_many_query_rows(D, G, Tq, dt):
     gen = torch.Generator().manual_seed(D + G * Tq)
     k, v = (kvref.Side(gen, 3, 2, D, 16, 32, 3, 300, per_slot=True) for _ in (0, 1))
     _run((1.5 * torch.randn(3, 2 * G, Tq, D, generator=gen)).to(dt), k, v, [(16, 270, 5, 32), (16, 299, 0, 2), (7, 0, 31, 9)])
+
+def test_a_dominating_middle_token_under_an_older_reference():
+    """Numerators of the middle are rounded to FP16 once, by up to half a step of 11 significant bits: 2^-11.  A token that
+    holds nearly all of the weight, 2^4 (1 + 0.51 2^-10) of the reference (under its limit of 2^5, so that the reference
+    stays), is rounded up by 0.49 2^-10, its share of the denominator not at all; the output's own rounding adds up to
+    half a step, in the same direction here."""
+    w = 16 * (1 + 0.51 * 2.0 ** -10)
+    key, value = torch.full((160,), 15, dtype=torch.uint8), torch.zeros(160, dtype=torch.uint8)
+    key[0], key[130], value[130] = 0, 2, 2                            # E2M1: -6 (far below) but for 0 and 1; 0 but for 1
+    scales = torch.full((1, 1, 160, 4), 0x38, dtype=torch.uint8)      # 1
+    scales[0, 0, key == 15] = 0x50                                    # 8: e^-133 of the first token's weight each
+    sides = []
+    # tokens 0 and 130 lie in the first and the fifth tile, which one warp takes; the result is 1 + 0.02 2^-10
+    for codes, g in ((key, 1.0), (value, (1 + w) / w * (1 + 0.02 * 2.0 ** -10))):
+        s = kvref.Side(torch.Generator().manual_seed(0), 1, 1, 64, 0, 16, 1, 160, rotate=False)
+        s.codes, s.scales, s.gscale = torch.zeros_like(s.codes), scales, torch.tensor([g])
+        s.codes[..., 0] = codes                                       # channel 0
+        sides.append(s)
+    q = torch.zeros(1, 1, 1, 64, dtype=F16)
+    q[..., 0] = 1
+    scale = math.log(w)
+    out, lse = nv.kv_attention(q.cuda(), *(s.store(nv) for s in sides), (0, 160, 0, 0), scale=scale, splits=1, want_lse=True)
+    want, l, _, _ = kvref.attention(q, *sides, [(0, 160, 0, 0)], scale=scale)
+    assert abs(float(want[..., 0]) - (1 + 0.02 * 2.0 ** -10)) < 2.0 ** -22 and not want[..., 1:].any()
+    off = (out.cpu().double() - want).abs()
+    assert (off <= want * (2.0 ** -11 + 2.0 ** -17) * (1 + 2.0 ** -10) + 2.0 ** -11).all(), float(off.max())
+    assert not out[..., 1:].any() and abs(float(lse) - float(l)) < 2.0 ** -19    # scores of 4 in FP32
