@@ -203,7 +203,9 @@ def append_many(caches, ks) -> None:
 def attend(q: torch.Tensor, k_cache: NVFP4KVCache, v_cache: NVFP4KVCache, causal: bool = True,
            scale: float | None = None, want_lse: bool = False, out: torch.Tensor | None = None):
     """Attention of the newest Tq tokens (already appended to both caches) over everything the caches hold: q
-    [B, Hq, Tq, D] (BF16 or FP16, Hq a multiple of the caches' heads), kv_attention's output(s)."""
+    [B, Hq, Tq, D] (BF16 or FP16, Hq a multiple of the caches' heads), kv_attention's output(s).  The lengths are the
+    caches' at the call: one captured into a CUDA graph keeps them (give kv_attention lengths on the device, or use
+    NVFP4PagedKVCache, where they change)."""
     a, b = ((c.n_sink, c.n_mid, c.head, c.n_window) for c in (k_cache, v_cache))
     if a != b:
         raise ValueError("the K and V caches hold different tokens")
@@ -229,9 +231,14 @@ def _append_records(recs: np.ndarray, f_lo: int, f_hi: int, device: torch.device
         _launch(device, fn, part.ctypes.data, len(part), f_lo, f_hi)
 
 
+def _capturing(device: torch.device) -> bool:
+    """Whether calls on the current stream go into a CUDA graph instead of running."""
+    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
 class DecodeStep:
     """n new tokens of some sequences of an NVFP4PagedKVCache, as `step` reserved them: `slots` (host), `slot_ids`
-    (device int32 [B]) and where their rows go in the windows."""
+    (device int32 [B], not to be written) and where their rows go in the windows."""
 
     def __init__(self, slots, n, slot_ids, rows, at, max_mid):
         self.slots, self.n, self.slot_ids, self._rows, self._at, self.max_mid = slots, n, slot_ids, rows, at, max_mid
@@ -249,6 +256,10 @@ class NVFP4PagedKVCache:
     Every sequence has its own tensor scales, fixed by its prefill and inherited by its forks.  Full pages of a
     forked sequence are shared (counted), its half-filled last page is copied, so a page with two owners is
     never written.  All calls of one cache belong on one stream.
+
+    store and attend may be captured into a CUDA graph, for all layers or some.  A replay serves the captured step's
+    sequences, in its order and with its n, as their lengths and pages are then: call step(slots, n) with those before each
+    replay (the other calls keep books on the host and cannot be captured).
 
     Attributes (device tensors):
       codes  [layers, 2, pages, H, page_tokens, D/2]   scales [..., D/16]   (2: K, V)
@@ -287,6 +298,7 @@ class NVFP4PagedKVCache:
         self._free = list(range(pages))                    # a heap: the lowest page first
         self._stores: dict[int, tuple[KvStore, KvStore]] = {}
         self._stores_of = None
+        self._captured: list[torch.Tensor] = []           # slot ids that CUDA graphs read, for the cache's life
 
     # ---- sequences ----
     @property
@@ -307,6 +319,7 @@ class NVFP4PagedKVCache:
 
     def free(self, slot: int) -> None:
         """End a sequence: its slot and the pages that no other sequence shares are free again."""
+        self._on_host("free")
         self._owned(slot)
         self._release(slot)
         self._held[slot] = None
@@ -316,6 +329,7 @@ class NVFP4PagedKVCache:
     def prefill(self, slot: int, ks, vs) -> None:
         """Start sequence `slot` (from alloc) from its prompt: ks[l], vs[l] [H, T, D] or [1, H, T, D] BF16, T >= sink +
         recent, rotary positions applied.  Tensor scales over the middle as NVFP4KVCache.prefill, per layer and side."""
+        self._on_host("prefill")
         if self._owned(slot) or self._lens[slot].any():
             raise RuntimeError("the sequence has been started")
         sides = [[self._prompt(x) for x in xs] for xs in (ks, vs)]
@@ -349,6 +363,7 @@ class NVFP4PagedKVCache:
     def fork(self, slot: int, n: int = 1) -> list[int]:
         """n new sequences that continue `slot`: its full pages are shared, the last page (when half filled) and the
         BF16 ends are copied, in one launch each."""
+        self._on_host("fork")
         held = self._owned(slot)
         free = [s for s, h in enumerate(self._held) if h is None]
         if n < 0 or len(free) < n:
@@ -382,6 +397,7 @@ class NVFP4PagedKVCache:
     def compact(self) -> int:
         """Moves the pages in use to the front of the pool, in one launch; returns their number (the pages from there
         on hold nothing)."""
+        self._on_host("compact")
         used = [p for p, r in enumerate(self._refs) if r]
         n = len(used)
         holes = [p for p in range(n) if not self._refs[p]]
@@ -405,6 +421,7 @@ class NVFP4PagedKVCache:
         """Reserve n (at most `recent`) new tokens for each of the distinct sequences `slots`: windows without room flush
         their oldest `recent` tokens into pages (64 rows of one layer and side each per launch), and the lengths on the
         device count the new tokens from here on."""
+        self._on_host("step")
         slots, r = [int(s) for s in slots], self.recent
         if len(set(slots)) != len(slots):
             raise ValueError("a sequence appears twice")
@@ -442,8 +459,17 @@ class NVFP4PagedKVCache:
         for x in (k, v):                             # both before the first is written
             if x.shape != shape or x.dtype != torch.bfloat16 or x.device != self.device:
                 raise ValueError(f"k and v must be bfloat16 {list(shape)} on {self.device}")
+        rows, at = self._places(step) if _capturing(self.device) else (step._rows, step._at)
         for side, x in enumerate((k, v)):
-            self.window[layer, side][step._rows, :, step._at] = x.detach().transpose(1, 2)
+            self.window[layer, side][rows, :, at] = x.detach().transpose(1, 2)
+
+    def _places(self, step: DecodeStep) -> tuple[torch.Tensor, torch.Tensor]:
+        """Where a step's rows go, from the lengths on the device: a graph's replay follows those of its own step."""
+        self._keep(step)
+        ids = step.slot_ids.long()
+        _, _, head, n_window = self.lens[ids].long()[:, :, None].unbind(1)
+        at = (head + n_window - step.n + torch.arange(step.n, device=self.device)) % (2 * self.recent)
+        return ids[:, None], at
 
     def attend(self, step: DecodeStep, layer: int, q: torch.Tensor, scale: float | None = None, causal: bool = True,
                want_lse: bool = False, out: torch.Tensor | None = None):
@@ -451,6 +477,8 @@ class NVFP4PagedKVCache:
         k, v = self.stores(layer)
         if q.shape[0] != len(step.slots) or q.shape[2] != step.n:
             raise ValueError("q must be [B, Hq, n, D] of the step")
+        if _capturing(self.device):
+            self._keep(step)
         return kv_attention(q, k, v, self.lens, self.table, step.slot_ids, causal, scale, step.max_mid, want_lse, out)
 
     def stores(self, layer: int) -> tuple[KvStore, KvStore]:
@@ -466,6 +494,15 @@ class NVFP4PagedKVCache:
         return self._stores[layer]
 
     # ---- bookkeeping ----
+    def _keep(self, step: DecodeStep) -> None:
+        """A captured step's slot ids outlive the step: the graph reads them at every replay."""
+        if not any(t is step.slot_ids for t in self._captured):
+            self._captured.append(step.slot_ids)
+
+    def _on_host(self, name: str) -> None:
+        if _capturing(self.device):
+            raise RuntimeError(f"{name} keeps books on the host: call it outside the capture, before each replay")
+
     def _owned(self, slot: int) -> list[int]:
         if not 0 <= slot < self.n_slots or self._held[slot] is None:
             raise ValueError(f"slot {slot} holds no sequence")

@@ -216,3 +216,41 @@ def test_a_pool_without_pages_still_needs_the_tensor_scale(L, side):
     none = dict(paged, table_cols=0, pages=0, Hq=1 << 30, Hkv=1, Tq=4)
     assert L.nvfp4_kv_attention(ctypes.byref(_desc(**{side: dict(gscale=None, codes=None, scales=None)}, **none)), 1, None, 0,
                                 None) == SIZE
+
+
+# ---- the paged cache under capture (see test_gpu_decode_graphs for the graphs themselves) ----
+def test_books_are_not_kept_in_a_graph(log, monkeypatch):
+    """Calls that change the host's lengths and pages are refused while a graph is captured, and change nothing."""
+    c = _cache()
+    s, e = c.alloc(), c.alloc()
+    c.prefill(s, _prompt(100), _prompt(100))
+    before, free = c._lens.copy(), c.pages_free
+    monkeypatch.setattr(kc, "_capturing", lambda d: True)
+    for call in (lambda: c.step([s]), lambda: c.free(s), lambda: c.fork(s), lambda: c.compact(),
+                 lambda: c.prefill(e, _prompt(100), _prompt(100))):
+        with pytest.raises(RuntimeError, match="capture"):
+            call()
+    assert (c._lens == before).all() and c.pages_free == free and c._held[s] == [0, 1, 2] and not log["copies"]
+
+
+@pytest.mark.parametrize("n", [1, 3, 16])
+def test_captured_rows_go_where_the_lengths_on_the_device_say(log, monkeypatch, n):
+    """store's captured form, run with each step's lengths and the FIRST step's object, against store with each step's
+    own: the same windows, through flushes and around the ring."""
+    a, b = _cache(pages=40), _cache(pages=40)
+    for c in (a, b):
+        for T in (32, 32 + 20, 32 + 7):
+            c.prefill(c.alloc(), _prompt(T), _prompt(T))
+    first = b.step([2, 0], n)
+    for i in range(20):
+        st = a.step([2, 0], n)
+        if i:
+            b.step([2, 0], n)
+        for layer in range(2):
+            x = torch.randn(2, H, n, D).to(BF)
+            a.store(st, layer, x, -x)
+            with monkeypatch.context() as m:
+                m.setattr(kc, "_capturing", lambda d: True)
+                b.store(first, layer, x, -x)
+        assert torch.equal(a.window, b.window) and torch.equal(a.lens, b.lens)
+    assert any(t is first.slot_ids for t in b._captured)              # kept for the graph that reads it
