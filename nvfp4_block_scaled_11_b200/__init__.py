@@ -1074,6 +1074,8 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
     position (rope_frequencies); channels from rot on pass unchanged.  Pairs are (i, i + rot/2), or (2i, 2i + 1) when
     interleaved.  inverse=True turns back: with the same mscale the adjoint, the gradient's pass.
     out: None (new contiguous tensors), or what x is, with the same shapes; x itself for in place.
+    Gradients reach x (by the inverse), not positions or freqs; a call with out= records none and is refused where one is
+    asked for.
     Returns a tensor, or a list for a sequence."""
     one = isinstance(x, torch.Tensor)
     xs = [x] if one else list(x)
@@ -1100,6 +1102,14 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
     pos_shape, ps = positions.shape, positions.stride()
     if pos_shape not in ((T,), (B, T)) or positions.device != dev:
         raise ValueError("positions must be [T] or [B, T] on x's device")
+    if torch.is_grad_enabled():
+        if freqs.requires_grad:
+            raise ValueError("freqs get no gradient: detach them")
+        if any(a.requires_grad for a in (*xs, *outs) if a is not None):
+            if given:
+                raise ValueError("a call with out= records no gradient: call it under no_grad, or without out")
+            outs = list(_Rope.apply(positions, freqs, interleaved, mscale, inverse, *xs))
+            return outs[0] if one else outs
     descs = []
     for j, a in enumerate(xs):
         if j:
@@ -1128,6 +1138,24 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
             1 if positions.dtype == torch.int64 else 0, ps[0] if len(ps) == 2 else 0, ps[-1], freqs.data_ptr(), mscale,
             1 if inverse else 0)
     return outs[0] if one else outs
+
+
+class _Rope(torch.autograd.Function):
+    """rope with its gradient: the map is linear in x and its adjoint is the inverse with the same mscale."""
+
+    @staticmethod
+    def forward(ctx, positions, freqs, interleaved, mscale, inverse, *xs):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions, freqs)
+        ctx.how = (interleaved, mscale, not inverse)
+        return tuple(rope(xs, positions, freqs, interleaved, mscale, inverse))
+
+    @staticmethod
+    def backward(ctx, *grads):
+        need = [n and g is not None for n, g in zip(ctx.needs_input_grad[5:], grads)]
+        gs = [g if g.shape[-1] < 2 or g.stride(-1) == 1 else g.contiguous() for g, n in zip(grads, need) if n]
+        got = iter(rope(gs, *ctx.saved_tensors, *ctx.how) if gs else ())
+        return (None,) * 5 + tuple(next(got) if n else None for n in need)
 
 
 class _PagesArray(ctypes.Structure):
