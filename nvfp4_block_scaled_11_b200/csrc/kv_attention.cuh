@@ -272,15 +272,33 @@ __device__ __forceinline__ int ka_units(const KaSeq& q) {
 struct KaParts {
   int64_t base, rem;                    // part c starts at c base + min(c, rem)
   int n;
-  __device__ __forceinline__ KaParts(int64_t total, int most) {
+  __host__ __device__ __forceinline__ KaParts(int64_t total, int most) {
     n = (int)min((int64_t)most, max(total / kKaMinUnits, (int64_t)1));
     base = total / n;
     rem = total - base * n;
   }
-  __device__ __forceinline__ int64_t start(int c) const { return c * base + min((int64_t)c, rem); }
-  __device__ __forceinline__ int of(int64_t u) const {
+  __host__ __device__ __forceinline__ int64_t start(int c) const { return c * base + min((int64_t)c, rem); }
+  __host__ __device__ __forceinline__ int of(int64_t u) const {
     return (int)(u < rem * (base + 1) ? u / (base + 1) : rem + (u - rem * (base + 1)) / base);
   }
+};
+// What a part that has come to unit u (before its end u_end) does of the job there, one of a sequence whose jobs begin at
+// seq_start and cost `cost` units each.
+struct KaPiece {
+  int job, first, last, units;          // units of work [first, last) of the job's
+  int64_t next;                         // the job's end
+  bool mine;                            // false: only units of starting the job are left, the next part begins it
+  __host__ __device__ __forceinline__ KaPiece(int64_t u, int64_t u_end, int64_t seq_start, int cost) {
+    job = (int)((u - seq_start) / cost);
+    units = cost - kKaJobUnits;
+    const int64_t work = seq_start + (int64_t)job * cost + kKaJobUnits;
+    mine = u_end > work;
+    first = (int)max(u - work, (int64_t)0);
+    last = (int)min((int64_t)units, u_end - work);
+    next = work + units;
+  }
+  __host__ __device__ __forceinline__ bool begun() const { return first == 0; }
+  __host__ __device__ __forceinline__ bool done() const { return last == units; }
 };
 
 template <bool BF>
@@ -374,11 +392,10 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
       sq = ka_sequence(p, ++b);
       cost = ka_units(sq);
     }
-    const int job = (int)((u - seq_start) / cost), units = cost - kKaJobUnits;
-    const int64_t job_work = seq_start + (int64_t)job * cost + kKaJobUnits;
-    if (u_end <= job_work) break;                                     // the next part begins the job
-    const int first_unit = (int)max(u - job_work, (int64_t)0), last_unit = (int)min((int64_t)units, u_end - job_work);
-    u = job_work + units;
+    const KaPiece piece(u, u_end, seq_start, cost);
+    if (!piece.mine) break;
+    const int job = piece.job, units = piece.units, first_unit = piece.first, last_unit = piece.last;
+    u = piece.next;
     const int kvh = job / p.row_tiles, row_tile = job - kvh * p.row_tiles;
     const int mid_units = ka_mid_units(sq), tiles = (sq.nm + kKaTile - 1) / kKaTile;
     const int t_first = min(first_unit, mid_units) * kKaWarps + w, t_end = min(tiles, min(last_unit, mid_units) * kKaWarps);
@@ -580,7 +597,7 @@ __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT =
     }
     if (gridDim.x > 1 && tid == kKaWarps * 32 - 1) {   // (the last warps have no query row of most calls)
       int4* e = p.ws_meta + (p.by_job ? (int64_t)b * jobs_per_seq + job : part);
-      const bool begun = first_unit == 0, done = last_unit == units;
+      const bool begun = piece.begun(), done = piece.done();
       if (begun && !done) *reinterpret_cast<int2*>(e) = make_int2(b, job), e->z = part;
       if (p.by_job ? done : begun && !done) e->w = p.by_job ? (begun ? -1 : part) : parts.of(u - 1);
     }
