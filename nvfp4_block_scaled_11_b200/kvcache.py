@@ -85,7 +85,7 @@ class NVFP4KVCache:
 
     def prefill(self, k: torch.Tensor) -> None:
         """Start the cache from K[B, H, T, D] (BF16), T >= sink + recent: the tensor scale over the rotated
-        middle, the middle quantized into rows 0 .. T - sink - recent - 1, sink and window verbatim."""
+        middle (over the whole prompt when it has none), the middle quantized into rows 0 .. T - sink - recent - 1, sink and window verbatim."""
         B, H, T, D = k.shape
         if (B, H, D) != (self.B, self.H, self.D) or k.dtype != torch.bfloat16:
             raise ValueError("k must be bfloat16 [B, H, T, D] matching the cache")
@@ -96,7 +96,8 @@ class NVFP4KVCache:
         n_mid = T - s - r
         if n_mid > self.capacity:
             raise ValueError("prefill middle exceeds the cache capacity")
-        kv_gscale(k, s, r, self.rotate, out=self.gscale)
+        # a prompt without a middle sets the scale by all of its tokens (0 would quantize every later one to 0)
+        kv_gscale(k, s if n_mid else 0, r if n_mid else 0, self.rotate, out=self.gscale)
         if n_mid:
             kv_append(k, s, n_mid, self.gscale, self.codes, self.scales, 0, self.rotate, self.f_lo, self.f_hi,
                       self.tile_layout)

@@ -254,3 +254,16 @@ def test_captured_rows_go_where_the_lengths_on_the_device_say(log, monkeypatch, 
                 b.store(first, layer, x, -x)
         assert torch.equal(a.window, b.window) and torch.equal(a.lens, b.lens)
     assert any(t is first.slot_ids for t in b._captured)              # kept for the graph that reads it
+
+
+@pytest.mark.parametrize("T,ends", [(32, (0, 0)), (33, (16, 16)), (60, (16, 16))])
+def test_a_prompt_without_a_middle_sets_the_scale_by_all_of_it(monkeypatch, T, ends):
+    """Both caches: over an empty middle the scale would be 0, and every token quantized with it 0."""
+    seen = []
+    monkeypatch.setattr(kc, "kv_gscale", lambda k, s, r, rot, out: seen.append((s, r)))
+    monkeypatch.setattr(kc, "kv_append", lambda *a: None)
+    monkeypatch.setattr(kc, "_append_records", lambda *a: None)
+    one, many = kc.NVFP4KVCache(1, H, D, capacity=64, device="cpu"), _cache(layers=1)
+    one.prefill(torch.ones(1, H, T, D, dtype=BF))
+    many.prefill(many.alloc(), _prompt(T, 1), _prompt(T, 1))
+    assert seen == [ends] * 3

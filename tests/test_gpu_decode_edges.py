@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import nvfp4_block_scaled_11_b200 as nv
+from nvfp4_block_scaled_11_b200 import kvcache as kc
 from tests import kvref
 
 pytestmark = pytest.mark.gpu
@@ -142,3 +143,34 @@ def test_a_dominating_middle_token_under_an_older_reference():
     off = (out.cpu().double() - want).abs()
     assert (off <= want * (2.0 ** -11 + 2.0 ** -17) * (1 + 2.0 ** -10) + 2.0 ** -11).all(), float(off.max())
     assert not out[..., 1:].any() and abs(float(lse) - float(l)) < 2.0 ** -19    # scores of 4 in FP32
+
+
+def test_caches_that_start_without_a_middle():
+    """The shortest prompt, then tokens that fill pages: the contiguous cache against the definition, and the same bytes as
+    the paged one."""
+    gen = torch.Generator().manual_seed(22)
+    H, D, T = 2, 64, 32
+    rows = lambda n: torch.randn(1, H, n, D, generator=gen).to(BF).cuda()  # noqa: E731
+    k, v = rows(T), rows(T)
+    one = [kc.NVFP4KVCache(1, H, D, capacity=96) for _ in (0, 1)]
+    many = kc.NVFP4PagedKVCache(1, 1, H, D, 4, 32)
+    one[0].prefill(k), one[1].prefill(v)
+    many.prefill(many.alloc(), [k], [v])
+    for _ in range(70):
+        k, v = rows(1), rows(1)
+        one[0].append(k), one[1].append(v)
+        st = many.step([0])
+        many.store(st, 0, k, v)
+    q = torch.randn(1, 6, 1, D, generator=gen).to(BF)
+    out, lse = kc.attend(q.cuda(), *one, want_lse=True)
+    sides = []
+    for i, c in enumerate(one):
+        s = kvref.Side(gen, 1, H, D, 16, 32, 1, 96)
+        s.sink, s.window, s.codes, s.scales, s.gscale = (t.cpu() for t in (c.sink, c.window, c.codes, c.scales, c.gscale))
+        sides.append(s)
+        n = c.n_mid
+        assert n == 64 and float(s.gscale) > 0 and (s.codes[0, :, :n] != 0).any(2).all()
+        paged = many.codes[0, i, many.table[0, :2].long()].transpose(0, 1).flatten(1, 2).cpu()
+        assert torch.equal(paged[:, :n], s.codes[0, :, :n]) and float(many.gscale[0, i, 0]) == float(s.gscale)
+    c = one[0]
+    kvref.check(out, lse, kvref.attention(q, *sides, [(c.n_sink, c.n_mid, c.head, c.n_window)]))
