@@ -789,8 +789,13 @@ def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
 
 
 def _no_shared_elements(t: torch.Tensor, name: str) -> None:
-    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
-        raise ValueError(f"{name} must not be an expanded tensor (it is written)")
+    """An output's elements are written at the same time: none may be another's.  Every view that slicing, splitting and
+    transposing give has strides that pass the reach of the smaller ones; others are taken as overlapping."""
+    reach = 0
+    for s, n in sorted((s, n) for n, s in zip(t.shape, t.stride()) if n > 1):
+        if s <= reach and t.numel():
+            raise ValueError(f"{name} must not be an expanded tensor or one whose rows overlap (it is written)")
+        reach += (n - 1) * s
 
 
 def _extent(t: torch.Tensor) -> tuple[int, int]:

@@ -267,3 +267,27 @@ def test_a_prompt_without_a_middle_sets_the_scale_by_all_of_it(monkeypatch, T, e
     one.prefill(torch.ones(1, H, T, D, dtype=BF))
     many.prefill(many.alloc(), _prompt(T, 1), _prompt(T, 1))
     assert seen == [ends] * 3
+
+
+def test_outputs_that_overlap_themselves_are_told():
+    """By brute force over small strided views: accepted only where every element has its own place; everything that
+    slicing, transposing and splitting one buffer gives is accepted."""
+    import itertools
+    buf = torch.arange(400)
+    told = 0
+    for sizes in itertools.product((1, 2, 3), repeat=3):
+        for strides in itertools.product((0, 1, 2, 3, 5, 6, 9), repeat=3):
+            t = buf.as_strided(sizes, strides)
+            alone = len(set(t.flatten().tolist())) == t.numel()
+            try:
+                nv._no_shared_elements(t, "out")
+                assert alone, (sizes, strides)
+            except ValueError:
+                told += not alone
+    assert told > 1000
+    base = torch.zeros(4, 6, 10, 8)
+    for t in (base, base.transpose(1, 2), base[:, ::2], base[1:3, :, 2:9:3].permute(2, 0, 1, 3), base.unflatten(1, (2, 3))[:, 1],
+              base[:0], base[..., :1], base[:, :, :, 3:5].transpose(0, 2)):
+        nv._no_shared_elements(t, "out")
+    with pytest.raises(ValueError):                                  # windows that slide by less than their width
+        nv._no_shared_elements(torch.zeros(100).as_strided((4, 8), (4, 1)), "out")
