@@ -821,7 +821,7 @@ def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
     sizes = list(zip(a.shape, a.stride(), b.shape, b.stride()))
     e = a.element_size()
     off = b.data_ptr() - a.data_ptr()
-    if e != b.element_size() or off % e or any(na > 1 and nb > 1 and sa != sb for na, sa, nb, sb in sizes):
+    if a.dim() != b.dim() or e != b.element_size() or off % e or any(na > 1 and nb > 1 and sa != sb for na, sa, nb, sb in sizes):
         return True
     # b's element j is a's element i where sum (i_d - j_d) stride_d is the distance of their first ones
     dims = sorted(((sa if na > 1 else sb, 1 - nb, na - 1) for na, sa, nb, sb in sizes if (na > 1 or nb > 1) and (sa if na > 1 else sb)),
@@ -929,6 +929,7 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
     b is slot b.  causal: query i of Tq sees positions <= length - Tq + i.
     max_mid: a bound on the middle's length that sizes the work split when lens is on the device (any value
     gives a correct result).  splits / workspace: nvfp4_kv_attention_splits' choice and an own allocation by default.
+    out, lse and workspace share no memory with q or one another.  The result carries no gradient.
     Returns out [B, Hq, Tq, D] in q's dtype, or (out, lse float32 [B, Hq, Tq]) with want_lse."""
     _rows(q, "q")
     if q.dim() != 4:
@@ -989,6 +990,8 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
         _out(lse, "lse", torch.float32, B * Hq * Tq)
         if lse.device != dev:
             raise ValueError("lse must be on q's device")
+        if _overlap(lse, q) or _overlap(lse, out):
+            raise ValueError("lse must not overlap q or out")
     elif want_lse:
         lse = q.new_empty((B, Hq, Tq), dtype=torch.float32)
     if splits is None:
@@ -1003,6 +1006,8 @@ def kv_attention(q: torch.Tensor, k: KvStore, v: KvStore, lens, table: torch.Ten
         _cuda(workspace, "workspace")
         if workspace.device != dev or workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace must hold {need} bytes on q's device")
+        if any(_overlap(workspace, t) for t in (q, out, lse) if t is not None):
+            raise ValueError("workspace must not overlap q, out or lse")
     q_sb, q_sh, q_st, _ = q.stride()
     o_sb, o_sh, o_st, _ = out.stride()
     desc = _KV_ATTENTION.pack(

@@ -291,3 +291,9 @@ def test_outputs_that_overlap_themselves_are_told():
         nv._no_shared_elements(t, "out")
     with pytest.raises(ValueError):                                  # windows that slide by less than their width
         nv._no_shared_elements(torch.zeros(100).as_strided((4, 8), (4, 1)), "out")
+
+
+def test_views_of_other_dims_are_taken_by_their_span():
+    buf = torch.zeros(64)
+    a = buf[:32].view(2, 4, 4)
+    assert nv._overlap(a, buf[16:48]) and nv._overlap(buf[31:40], a) and not nv._overlap(a, buf[32:]) and nv._overlap(a, buf[8:9])

@@ -174,3 +174,24 @@ def test_caches_that_start_without_a_middle():
         assert torch.equal(paged[:, :n], s.codes[0, :, :n]) and float(many.gscale[0, i, 0]) == float(s.gscale)
     c = one[0]
     kvref.check(out, lse, kvref.attention(q, *sides, [(c.n_sink, c.n_mid, c.head, c.n_window)]))
+
+
+def test_written_buffers_share_no_memory():
+    """lse and workspace inside q, out or each other are refused; side by side in one buffer they are not."""
+    gen = torch.Generator().manual_seed(23)
+    k, v = (kvref.Side(gen, 2, 2, 64, 16, 32, 2, 100).store(nv) for _ in (0, 1))
+    lens = (16, 90, 0, 20)
+    need = nv.lib().nvfp4_kv_attention_workspace_bytes(2, 64, 4)
+    buf = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
+    at = lambda a, n, dt=BF: buf[a:a + n].view(dt)  # noqa: E731
+    q, out, lse, ws = at(0, 1024).view(2, 4, 1, 64), at(1024, 1024).view(2, 4, 1, 64), at(2048, 32, torch.float32), buf[3072:3072 + need]
+    q.copy_(torch.randn(2, 4, 1, 64, generator=gen))
+    want, wl = nv.kv_attention(q.clone(), k, v, lens, splits=4, want_lse=True)
+    nv.kv_attention(q, k, v, lens, splits=4, out=out, lse=lse, workspace=ws)
+    assert torch.equal(out, want) and torch.equal(lse.view(2, 4, 1), wl)
+    for kw in (dict(lse=at(64, 32, torch.float32)), dict(lse=at(1024 + 992, 32, torch.float32)), dict(workspace=buf[1024:]),
+               dict(workspace=buf[:need]), dict(workspace=buf[2064:]), dict(workspace=buf[:need].view(BF)),
+               dict(lse=lse.view(2, 4, 1), workspace=buf[2064:2064 + need].view(torch.float32))):
+        with pytest.raises(ValueError, match="overlap"):
+            nv.kv_attention(q, k, v, lens, splits=4, **(dict(out=out, lse=lse, workspace=ws) | kw))
+    assert torch.equal(out, want)
