@@ -217,6 +217,8 @@ def attend(q: torch.Tensor, k_cache: NVFP4KVCache, v_cache: NVFP4KVCache, causal
     return kv_attention(q, k_cache.store(), v_cache.store(), a, causal=causal, scale=scale, want_lse=want_lse, out=out)
 
 
+_MAX_MIDDLE = 2 ** 29 - 1      # tokens of a sequence's middle at most (nvfp4_kv_attention)
+
 # nvfp4_kv_append_desc as a numpy record, so that a flush over many layers and sequences is filled column by column
 _APPEND = np.dtype([("k_bf16", np.uint64), ("gscale", np.uint64), ("codes", np.uint64), ("scales", np.uint64),
                     *((n, np.int64) for n in ("BH", "T", "first", "n", "D", "cap", "t0")),
@@ -284,7 +286,8 @@ class NVFP4PagedKVCache:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
-        cols = pages if max_tokens is None else min(pages, max(-(-max_tokens // page_tokens), 1))
+        # (attention counts positions in 32 bits: a table of more columns than a sequence can fill is refused there)
+        cols = min(pages if max_tokens is None else max(-(-max_tokens // page_tokens), 1), pages, max(_MAX_MIDDLE // page_tokens, 1))
         z = lambda *s, dt=torch.uint8: torch.zeros(s, dtype=dt, device=dev)  # noqa: E731
         self.codes, self.scales = (z(layers, 2, pages, H, page_tokens, D // w) for w in (2, 16))
         self.sink = z(layers, 2, slots, H, sink, D, dt=torch.bfloat16)

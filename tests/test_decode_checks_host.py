@@ -297,3 +297,14 @@ def test_views_of_other_dims_are_taken_by_their_span():
     buf = torch.zeros(64)
     a = buf[:32].view(2, 4, 4)
     assert nv._overlap(a, buf[16:48]) and nv._overlap(buf[31:40], a) and not nv._overlap(a, buf[32:]) and nv._overlap(a, buf[8:9])
+
+
+def test_tables_of_large_pools_stay_within_what_attention_takes(L):
+    """A pool of more tokens than one sequence may have: its table has the columns that attention accepts, not one per page."""
+    c = kc.NVFP4PagedKVCache(1, 1, 1, 64, 1000, 1 << 20, device="meta")
+    assert c.table.shape == (1, 511)
+    paged = dict(table=0x80000, lens=0x90000, page_rows=1 << 20, pages=1000, Hkv=1)
+    assert L.nvfp4_kv_attention(ctypes.byref(_desc(**paged, table_cols=512)), 1, None, 0, None) == SIZE
+    # the table is accepted: what is refused is the missing q
+    assert L.nvfp4_kv_attention(ctypes.byref(_desc(**paged, table_cols=511, q=None)), 1, None, 0, None) == ARG
+    assert kc.NVFP4PagedKVCache(1, 1, 1, 64, 1000, 64, device="meta").table.shape == (1, 1000)
