@@ -1115,9 +1115,10 @@ def rope(x, positions, freqs: torch.Tensor, interleaved: bool = False, mscale: f
     if torch.is_grad_enabled():
         if freqs.requires_grad:
             raise ValueError("freqs get no gradient: detach them")
-        if any(a.requires_grad for a in (*xs, *outs) if a is not None):
-            if given:
-                raise ValueError("a call with out= records no gradient: call it under no_grad, or without out")
+        asked = [a for a in (xs + outs if given else xs) if a.requires_grad]
+        if asked and given:
+            raise ValueError("a call with out= records no gradient: call it under no_grad, or without out")
+        if asked:
             outs = list(_Rope.apply(positions, freqs, interleaved, mscale, inverse, *xs))
             return outs[0] if one else outs
     descs = []

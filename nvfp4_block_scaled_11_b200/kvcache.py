@@ -34,7 +34,7 @@ from . import (KV_APPEND_BATCH_MAX, KvAppendBatch, KvStore, _KvAppendDesc, _laun
 def _buffers(c) -> tuple:
     """Where a cache's buffers are: its KvStores are made anew when one has been replaced.  (A KvStore keeps what it reads
     alive, so a replacement never has the old one's address.)"""
-    return (*(t.data_ptr() for t in (c.sink, c.window, c.codes, c.scales, c.gscale)), c.rotate)
+    return c.sink.data_ptr(), c.window.data_ptr(), c.codes.data_ptr(), c.scales.data_ptr(), c.gscale.data_ptr(), c.rotate
 
 
 class NVFP4KVCache:
@@ -234,11 +234,6 @@ def _append_records(recs: np.ndarray, f_lo: int, f_hi: int, device: torch.device
         _launch(device, fn, part.ctypes.data, len(part), f_lo, f_hi)
 
 
-def _capturing(device: torch.device) -> bool:
-    """Whether calls on the current stream go into a CUDA graph instead of running."""
-    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
-
-
 class DecodeStep:
     """n new tokens of some sequences of an NVFP4PagedKVCache, as `step` reserved them: `slots` (host), `slot_ids`
     (device int32 [B], not to be written) and where their rows go in the windows."""
@@ -302,6 +297,7 @@ class NVFP4PagedKVCache:
         self._free = list(range(pages))                    # a heap: the lowest page first
         self._stores: dict[int, tuple[KvStore, KvStore]] = {}
         self._stores_of = None
+        self._capturing = torch.cuda.is_current_stream_capturing if dev.type == "cuda" else bool   # (bool() is False)
         self._captured: list[torch.Tensor] = []           # slot ids that CUDA graphs read, for the cache's life
 
     # ---- sequences ----
@@ -463,7 +459,7 @@ class NVFP4PagedKVCache:
         for x in (k, v):                             # both before the first is written
             if x.shape != shape or x.dtype != torch.bfloat16 or x.device != self.device:
                 raise ValueError(f"k and v must be bfloat16 {list(shape)} on {self.device}")
-        rows, at = self._places(step) if _capturing(self.device) else (step._rows, step._at)
+        rows, at = self._places(step) if self._capturing() else (step._rows, step._at)
         for side, x in enumerate((k, v)):
             self.window[layer, side][rows, :, at] = x.detach().transpose(1, 2)
 
@@ -481,7 +477,7 @@ class NVFP4PagedKVCache:
         k, v = self.stores(layer)
         if q.shape[0] != len(step.slots) or q.shape[2] != step.n:
             raise ValueError("q must be [B, Hq, n, D] of the step")
-        if _capturing(self.device):
+        if self._capturing():
             self._keep(step)
         return kv_attention(q, k, v, self.lens, self.table, step.slot_ids, causal, scale, step.max_mid, want_lse, out)
 
@@ -504,7 +500,7 @@ class NVFP4PagedKVCache:
             self._captured.append(step.slot_ids)
 
     def _on_host(self, name: str) -> None:
-        if _capturing(self.device):
+        if self._capturing():
             raise RuntimeError(f"{name} keeps books on the host: call it outside the capture, before each replay")
 
     def _owned(self, slot: int) -> list[int]:

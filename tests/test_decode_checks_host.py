@@ -225,7 +225,7 @@ def test_books_are_not_kept_in_a_graph(log, monkeypatch):
     s, e = c.alloc(), c.alloc()
     c.prefill(s, _prompt(100), _prompt(100))
     before, free = c._lens.copy(), c.pages_free
-    monkeypatch.setattr(kc, "_capturing", lambda d: True)
+    monkeypatch.setattr(c, "_capturing", lambda: True)
     for call in (lambda: c.step([s]), lambda: c.free(s), lambda: c.fork(s), lambda: c.compact(),
                  lambda: c.prefill(e, _prompt(100), _prompt(100))):
         with pytest.raises(RuntimeError, match="capture"):
@@ -250,7 +250,7 @@ def test_captured_rows_go_where_the_lengths_on_the_device_say(log, monkeypatch, 
             x = torch.randn(2, H, n, D).to(BF)
             a.store(st, layer, x, -x)
             with monkeypatch.context() as m:
-                m.setattr(kc, "_capturing", lambda d: True)
+                m.setattr(b, "_capturing", lambda: True)
                 b.store(first, layer, x, -x)
         assert torch.equal(a.window, b.window) and torch.equal(a.lens, b.lens)
     assert any(t is first.slot_ids for t in b._captured)              # kept for the graph that reads it
