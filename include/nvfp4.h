@@ -408,7 +408,8 @@ typedef struct nvfp4_kv_store {
 typedef struct nvfp4_kv_attention_desc {
   const void* q;            /* [B, Hq, Tq, D] at the given strides (elements; channels contiguous), dtype */
   void* out;                /* the same shape and dtype at its own strides; must not overlap q */
-  float* lse;               /* NULL, or [B, Hq, Tq] contiguous: log of the softmax denominators (natural log) */
+  float* lse;               /* NULL, or [B, Hq, Tq] contiguous: log of the softmax denominators (natural log); must not
+                               overlap q or out */
   int64_t q_sb, q_sh, q_st, out_sb, out_sh, out_st;
   int64_t B, Hq, Hkv, Tq, D;          /* D: 64, 128 or 256; Hq a multiple of Hkv: query head h reads K/V head
                                          h / (Hq / Hkv) */
@@ -432,7 +433,7 @@ typedef struct nvfp4_kv_attention_desc {
 /* out = softmax(scale q K^T) V over the tokens of each sequence in the order sink | middle | window (slots head,
  * head + 1, ... of the ring).  A row that sees no token gets zeros and lse -Inf.  Middle tokens stand for
  * E2M1(code) * E4M3(scale) * g, un-rotated when `rotate`; sums and softmax statistics are FP32, the middle's
- * query is carried in 22 bits and its numerators in FP16 (scaled by 2^10), the BF16 ends' in 16 bits.
+ * query is carried in 22 bits and its numerators in FP16 (11 bits, scaled by 2^10), the BF16 ends' in 16 bits.
  * Hidden tokens (past a row's position, past a sequence's end) reach no row, whatever they hold; a visible
  * NaN reaches the rows that see it.
  * splits: the number of parts (1 .. 65535), one per CTA, that all the call's tokens are cut into evenly, whatever the
@@ -490,7 +491,8 @@ typedef struct nvfp4_pages_array {
 /* Copies page src[j] to page dst[j], j < n, in every one of `count` (at most NVFP4_PAGES_MAX) arrays: forking a
  * sequence, copying on write, compacting a pool.  src and dst are HOST arrays, read before the call returns.
  * All pairs move at once: every dst is distinct and none of them is a src (NVFP4_ERR_ARG otherwise, as for an
- * index outside the smallest array's pages; nothing is enqueued).  One launch per 1024 pairs. */
+ * index outside the smallest array's pages; nothing is enqueued).  The arrays must not overlap one another.  One launch
+ * per 1024 pairs. */
 int nvfp4_copy_pages(const nvfp4_pages_array* arrays, int count, const int32_t* src, const int32_t* dst, int64_t n,
                      void* stream);
 

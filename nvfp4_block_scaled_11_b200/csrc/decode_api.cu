@@ -67,7 +67,8 @@ int launch_kv_attention_d(const KvAttnParams& p, bool bf, int nt, unsigned parts
 
 // Query rows of a CTA in units of 8: one K/V head's rows fit 8 for most decode steps; more rows share the
 // expansion of the codes in tiles of 16.  16 sequences of 8192 tokens, 2 K/V heads, 16 rows, tiles of 16 against 8 (us):
-// D = 64 21.1 / 22.1, D = 128 26.0 / 28.2, D = 256 42.0 / 45.0; 64 rows, D = 128: 69.1 / 82.0.
+// D = 64 17.9 / 20.4, D = 128 24.1 / 27.0, D = 256 41.6 / 44.0; 64 rows: 41.8 / 54.8, 62.4 / 78.9, 111.4 / 136.6.  Every
+// tile expands the whole cache again, so many rows are far from the bytes' time (5.8 us at D = 128).
 int ka_row_units(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 // CTAs of the attention kernel that an SM holds (its launch bounds and shared memory).
@@ -116,7 +117,9 @@ int nvfp4_kv_attention_splits(int64_t B, int64_t Hkv, int64_t rows, int64_t D, i
   const int64_t slots = (int64_t)sm_count() * ka_ctas_per_sm(D, nt);
   const int64_t work = checked_prod({jobs, units});
   if (jobs <= 0 || work < 0) return NVFP4_OK;
-  // short jobs (up to 4 units of work) that leave room for all of them at once keep a CTA each: nothing to join
+  // Short jobs (up to 4 units of work) that leave room for all of them at once keep a CTA each: nothing to join.  Against
+  // parts of kKaMinUnits (us, D = 128, 8 heads, 4 rows): 64 tokens 7.4 / 9.4, 301 tokens 8.8 / 10.1, 8 and 32 sequences of 301
+  // 8.9 / 10.4 and 10.0 / 13.7; just past it, 480 tokens (5 units of work) 10.2 / 10.8, 600 (6 units) 11.7 / 10.7.
   *splits = (int)(units <= 4 + kKaJobUnits && jobs <= slots ? jobs : std::min(slots, std::max<int64_t>(work / kKaMinUnits, 1)));
   return NVFP4_OK;
 }
@@ -260,7 +263,8 @@ int nvfp4_rope(const nvfp4_rope_tensor* tensors, int count, int64_t B, int64_t T
   // Tokens per CTA (of one sequence): as few as make one wave of CTAs, or two or more waves where its angles would pass
   // the shared memory.  A wave that is not full costs as much as a full one; 8192 tokens of 40 heads with tiles
   // of 8 (1.4 waves) / 10 / 12 (0.9) / 16 / 24: 34.8 / 37.8 / 31.4 / 33.6 / 39.4 us, 2 x 2047 tokens of 32 heads of 64 FP32
-  // channels with 4 / 6 (0.9) / 8 / 12: 16.8 / 15.0 / 16.0 / 18.7 us.
+  // channels with 4 / 6 (0.9) / 8 / 12: 16.8 / 15.0 / 16.0 / 18.7 us (into kept outputs; into new ones the
+  // chosen tiles take 32.6 to 32.9 and 15.4 to 15.6).
   const int64_t most = std::min<int64_t>(std::max<int64_t>(T, 1), std::min<int64_t>(32, half ? kRopeSmemPairs / half : 32));
   const int64_t wave = (int64_t)sms * kRopeCtasPerSm, waves = (B * T + wave * most - 1) / (wave * most);
   int64_t tile = std::max<int64_t>(1, (B * T + wave * waves - 1) / (wave * waves));

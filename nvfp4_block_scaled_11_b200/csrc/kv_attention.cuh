@@ -12,12 +12,14 @@
 // One pass over the tokens with a running maximum and sum (kv_attn_kernel); what a CTA did not finish of a
 // job (sequence, K/V head, tile of query rows) is joined by kv_attn_combine_kernel.  Bytes to move: 2 (D/2 + D/16) per
 // middle token and K/V head, which at the copy rate of a B200 (6549 GB/s) is 92.5 us for 16 sequences of
-// 32768 tokens, 8 K/V heads, D = 128; the kernel takes 140 us there, 4.3 TB/s.  It is not the bytes that bound it but
-// turning 4-bit codes into operands: per tile of 32 tokens a warp issues 623 instructions, of them 128 converts
-// (e2m1x2) and 128 multiplies (f16x2) that hold their pipe two cycles each and were measured not to overlap
-// (15.5 cycles per 4 + 4), and 48 products.  Counters at that size: 2.3 instructions per cycle and SM,
-// converts' pipe 43 %, FP16 23 %, tensor pipe 35 %, DRAM 51 %; of a warp's 2815 cycles per tile 20 wait for
-// copies, 820 issue them and 1880 compute.  The design keeps copies in flight and instructions per byte low:
+// 32768 tokens, 8 K/V heads, D = 128; the kernel takes 139 us there in a CUDA graph, 4.35 TB/s (back-to-back calls
+// 142 to 157).  Neither the bytes nor any one pipe is full: DRAM 54 %, issue slots 56 % (2.26 instructions per cycle and
+// SM), converts' pipe 43 %, FP16 23 %, tensor pipe 35 %; in 44 % of a scheduler's cycles none of its 2.8 warps is
+// eligible, and the largest stall is the fixed latency of the instruction before (1.3 cycles per instruction).  Latency
+// at three warps per scheduler bounds it: registers (159) allow no more, and a warp has 623 instructions per tile of 32
+// tokens, among them 128 converts (e2m1x2) and 128 multiplies (f16x2) of two cycles each and 48 products.  Of its 2815
+// cycles per tile 20 wait for copies, 820 go into issuing them and 1880 compute.  The design keeps copies in
+// flight and instructions per byte low:
 // * every warp owns its tiles of 32 tokens and its own ring of shared-memory stages filled by cp.async: no
 //   CTA-wide barrier inside the loop, rows behind the end arrive as zeros.  Bulk copies take the same bytes with
 //   one instruction per row group, but each lane's copy is issued by itself (78 cycles): 157 us issued by every
@@ -40,8 +42,8 @@
 // * the reference that numerators are taken against follows the maximum only when a score passes it by 2^5, so almost
 //   no tile rescales the accumulators;
 // * one job per CTA leaves SMs idle when sequences differ in length: all tokens of the call are cut evenly instead
-//   (see ka_units).  One sequence of 32768 tokens: 18.3 us; 48 of up to 8191: 46.8; 8 draft steps of 4 tokens,
-//   D = 64: 13.5; D = 256 with 16 query heads on one K/V head: 35.7; 301 tokens: 8.4 (of which launch, the query's
+//   (see ka_units).  In a graph: one sequence of 32768 tokens 18.4 us; 48 of up to 8191 47; 8 draft steps of 4 tokens,
+//   D = 64, 13.4; D = 256 with 16 query heads on one K/V head 35.7; 301 tokens 8.2 to 8.9 (of which launch, the query's
 //   rotation and three dependent rounds of loads are most).
 #pragma once
 
@@ -57,11 +59,17 @@ namespace nvfp4 {
 
 constexpr int kKaWarps = 4;            // warps per CTA, each with its own tiles
 constexpr int kKaTile = 32;            // middle tokens per tile
-// What starting and ending a job costs, in units of work (4 tiles).  Measured with 1 / 2 / 3 / 5 / 8 (us): 48 ragged sequences
-// 52.4 / 51.6 / 49.2 / 52.8 / 57.1, draft tokens 23.3 / 20.1 / 17.6 / 18.3 / 19.5, 16 sequences with D = 256 42.1 / 41.0 /
-// 36.9 / 35.9 / 38.1.
+// What starting and ending a job costs, in units of work (4 tiles).  Measured with 3 / 5 / 8 (us in a graph): 48 ragged
+// sequences 47.5 / 48.5 / 51.8, draft tokens 13.4 / 13.6 / 13.9, one long sequence 18.2 / 18.2 / 18.9, 16 sequences of
+// 32768 138.9 / 139.0 / 140.4, D = 256 with 16 rows, where a unit of work is longer, 35.6 / 33.6 / 36.8.  (1 and 2 were
+// slower in an earlier form, ragged 52.4 and 51.6 against 49.2.)
 constexpr int kKaJobUnits = 3;
-constexpr int kKaMinUnits = 4;         // least units per part: shorter ones cost more in joining than they win
+// Least units of a part.  At most one more than kKaJobUnits: whole jobs of the least work are then never cut, which the
+// host counts on.  Measured with 2 / 3 / 4 / 6 / 8 (us, D = 128, 4 rows): one sequence of 2048 tokens and 8 heads 9.2 / 9.8 /
+// 10.7 / 13.0 / 14.2, 4 of 1024 9.9 / 10.2 / 11.1 / 13.1 / 14.5; the draft tokens 12.7 / 13.0 / 13.4 / 15.5 / 17.2; calls
+// whose parts are longer anyway do not differ.  4 makes every part longer than a job's start, so that each has work of
+// its own; 2 and 3, faster here, would need that given up.
+constexpr int kKaMinUnits = 4;
 constexpr int kKaMaxSplits = 65535;
 constexpr int kKaJoinWarps = 8;        // warps that join the pieces of one query row
 constexpr float kKaPShift = 10.0f;     // numerators of the middle are scaled by 2^10 before FP16
@@ -308,8 +316,9 @@ __device__ __forceinline__ void ka_store(char* out, int64_t i, float x) {
 }
 
 // D: head_dim; NT: query rows / 8 of a CTA; QBF: q and out are BF16 (else FP16).
-// CTAs per SM: as many as registers allow without spills in the loop.  D = 128, NT = 1 with 3 (146 registers) against
-// 4 (128 registers, spills): one long sequence 21.0 / 24.0 us, ragged 46.7 / 49.2, large 144.9 / 148.0.
+// CTAs per SM: as many as registers allow.  D = 128, NT = 1 with 3 (159 registers, no spills) against 4 (128, 56 bytes
+// spilled): one long sequence 18.3 / 21.5 us, ragged 47.5 / 52.0, large 138.9 / 141.8.  D = 256, NT = 2 needs all 255
+// registers of two CTAs and spills 40 (BF16) or 72 (FP16) bytes; the other forms spill nothing.
 template <int D, int NT, bool QBF>
 __global__ void __launch_bounds__(kKaWarps * 32, D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3))
     kv_attn_kernel(const __grid_constant__ KvAttnParams p) {

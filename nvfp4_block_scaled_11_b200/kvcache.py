@@ -38,7 +38,8 @@ def _buffers(c) -> tuple:
 
 
 class NVFP4KVCache:
-    """K (or V) cache of B x H heads of dimension D with room for `capacity` NVFP4 middle tokens.
+    """K (or V) cache of B x H heads of dimension D (a multiple of 16; attention over it takes 64, 128 and 256) with room
+    for `capacity` NVFP4 middle tokens.
 
     Attributes (device tensors):
       sink   [B, H, sink, D] bf16      first tokens, verbatim
@@ -251,7 +252,8 @@ class NVFP4PagedKVCache:
             cache.store(step, layer, k, v)           # [B, H, n, D] BF16, rotary positions already applied
             o = cache.attend(step, layer, q)         # [B, Hq, n, D]
 
-    Every sequence has its own tensor scales, fixed by its prefill and inherited by its forks.  Full pages of a
+    D is a multiple of 16 to be filled, 64, 128 or 256 to be attended over.  Every sequence has its own tensor scales, fixed
+    by its prefill and inherited by its forks.  Full pages of a
     forked sequence are shared (counted), its half-filled last page is copied, so a page with two owners is
     never written.  All calls of one cache belong on one stream.
 
@@ -452,7 +454,8 @@ class NVFP4PagedKVCache:
         return DecodeStep(slots, n, ids, ids.long()[:, None], at, int(self._lens[slots, 1].max()) if slots else 0)
 
     def store(self, step: DecodeStep, layer: int, k: torch.Tensor, v: torch.Tensor) -> None:
-        """The step's K and V rows [B, H, n, D] (BF16) of one layer."""
+        """Write the step's K and V rows [B, H, n, D] (BF16) of one layer into the windows (what attention reads of a layer
+        is `stores(layer)`)."""
         shape = (len(step.slots), self.H, step.n, self.D)
         if not 0 <= layer < self.layers:
             raise IndexError("no such layer")
