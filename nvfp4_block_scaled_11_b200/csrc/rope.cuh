@@ -6,16 +6,16 @@
 // direction turns by -a_i: with the same mscale it is the adjoint, i.e. the gradient's pass.
 //
 // Each element is read and written once, so the kernel is bound by memory, or by latency when a call is small.  The
-// angle is formed in FP64 (positions reach millions, where an FP32 product is off by whole radians) and
-// reduced to a fraction of a turn before FP32 sincospi (that rounds it by up to 2^-25 half turns, 9.4e-8 radians, at any
-// position: about the FP32 sine's own error, and nothing beside BF16's or FP16's rounding); a CTA does that once per token and pair and keeps it in
-// shared memory for all heads of all tensors of the call.  Threads then walk (token, head) rows with 16-byte
-// accesses: a thread keeps its place in the row, so no index is divided in the loop, and its first rows are
-// fetched before the angles are computed.  Measured in a graph, into kept outputs and into new ones: 8192 tokens of
-// 32 + 8 heads, 128 channels, BF16: 31.8 and 32.6 to 32.9 us for 168 MB, 5.1 to 5.3 TB/s; 2 x 2047 tokens of 16 + 16 heads,
-// 64 channels, FP32, interleaved, 32 of them turning: 15.1 and 15.4 to 15.6 us for 67 MB; one token of 48 sequences: 2.9 to
-// 3.1 us, a launch and two dependent loads.  What is left is each CTA's start, which all CTAs of
-// a wave share: positions, frequencies, angles and the barrier, with one row per thread in flight.
+// angle is formed in FP64 (positions reach millions, where an FP32 product is off by whole radians) and reduced to a
+// fraction of a turn before FP32 sincospi (that rounds it by up to 2^-25 half turns, 9.4e-8 radians, at any position:
+// about the FP32 sine's own error, and nothing beside BF16's or FP16's rounding); a CTA does that once per token and
+// pair and keeps it in shared memory for all heads of all tensors of the call.  Threads then walk (token, head) rows
+// with 16-byte accesses: a thread keeps its place in the row, so no index is divided in the loop, and its first rows
+// are fetched before the angles are computed.  Measured in a graph, into kept outputs and into new ones: 8192 tokens
+// of 32 + 8 heads, 128 channels, BF16: 31.8 and 32.6 to 32.9 us for 168 MB, 5.1 to 5.3 TB/s; 2 x 2047 tokens of 16 +
+// 16 heads, 64 channels, FP32, interleaved, 32 of them turning: 15.1 and 15.4 to 15.6 us for 67 MB; one token of 48
+// sequences: 2.9 to 3.1 us, a launch and two dependent loads.  What is left is each CTA's start, which all CTAs of a
+// wave share: positions, frequencies, angles and the barrier, with one row per thread in flight.
 #pragma once
 
 #include "device.cuh"

@@ -86,7 +86,8 @@ class NVFP4KVCache:
 
     def prefill(self, k: torch.Tensor) -> None:
         """Start the cache from K[B, H, T, D] (BF16), T >= sink + recent: the tensor scale over the rotated
-        middle (over the whole prompt when it has none), the middle quantized into rows 0 .. T - sink - recent - 1, sink and window verbatim."""
+        middle (over the whole prompt when it has none), the middle quantized into rows
+        0 .. T - sink - recent - 1, sink and window verbatim."""
         B, H, T, D = k.shape
         if (B, H, D) != (self.B, self.H, self.D) or k.dtype != torch.bfloat16:
             raise ValueError("k must be bfloat16 [B, H, T, D] matching the cache")
@@ -252,10 +253,10 @@ class NVFP4PagedKVCache:
             cache.store(step, layer, k, v)           # [B, H, n, D] BF16, rotary positions already applied
             o = cache.attend(step, layer, q)         # [B, Hq, n, D]
 
-    D is a multiple of 16 to be filled, 64, 128 or 256 to be attended over.  Every sequence has its own tensor scales, fixed
-    by its prefill and inherited by its forks.  Full pages of a
-    forked sequence are shared (counted), its half-filled last page is copied, so a page with two owners is
-    never written.  All calls of one cache belong on one stream.
+    D is a multiple of 16 to be filled, 64, 128 or 256 to be attended over.  Every sequence has its own tensor
+    scales, fixed by its prefill and inherited by its forks.  Full pages of a forked sequence are shared (counted),
+    its half-filled last page is copied, so a page with two owners is never written.  All calls of one cache belong
+    on one stream.
 
     store and attend may be captured into a CUDA graph, for all layers or some.  A replay serves the captured step's
     sequences, in its order and with its n, as their lengths and pages are then: call step(slots, n) with those before each
