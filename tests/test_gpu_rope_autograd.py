@@ -48,7 +48,8 @@ def test_several_tensors_of_one_projection(dt):
     got = qkv.grad
     for w, a, n in ((wq, 0, Hq), (wk, Hq, Hk)):
         y, mag = _ref(w, pos, f, False, m, True)
-        assert ((view(got, a, n).cpu().double() - y).abs() <= mag * 2.0 ** -20 + HALF[dt] * (y.abs() + mag * 2.0 ** -20) + 2.0 ** -26).all()
+        # (below FP16's normal range a step is 2^-24: half of it is off whatever the value)
+        assert ((view(got, a, n).cpu().double() - y).abs() <= mag * 2.0 ** -20 + HALF[dt] * (y.abs() + mag * 2.0 ** -20) + 2.0 ** -25).all()
     assert torch.equal(view(got, Hq + Hk, Hk), wv)
 
 
