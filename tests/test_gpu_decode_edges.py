@@ -184,7 +184,7 @@ def test_written_buffers_share_no_memory():
     need = nv.lib().nvfp4_kv_attention_workspace_bytes(2, 64, 4)
     buf = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
     at = lambda a, n, dt=BF: buf[a:a + n].view(dt)  # noqa: E731
-    q, out, lse, ws = at(0, 1024).view(2, 4, 1, 64), at(1024, 1024).view(2, 4, 1, 64), at(2048, 32, torch.float32), buf[3072:3072 + need]
+    q, out, lse, ws = at(0, 1024).view(2, 4, 1, 64), at(1024, 1024).view(2, 4, 1, 64), at(2048, 32, torch.float32), buf[2560:2560 + need]
     q.copy_(torch.randn(2, 4, 1, 64, generator=gen))
     want, wl = nv.kv_attention(q.clone(), k, v, lens, splits=4, want_lse=True)
     nv.kv_attention(q, k, v, lens, splits=4, out=out, lse=lse, workspace=ws)
